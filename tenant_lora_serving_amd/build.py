@@ -1,9 +1,10 @@
-"""Build step for the HIP library (liblora.so, gfx950) next to this file.
+"""Build step for the HIP libraries (liblora.so and libstep.so, gfx950) next to this file.
 
     python -m tenant_lora_serving_amd.build
 
 Compiles every source under csrc/ with hipcc into objects under _build/ (in
-parallel) and links them into tenant_lora_serving_amd/liblora.so.  Packed FP32
+parallel) and links them into tenant_lora_serving_amd/liblora.so (the routed
+delta) and libstep.so (the serving-step operators).  Packed FP32
 instructions are turned off for the device code (-packed-fp32-ops): the
 compiler otherwise forms them from plain float code.
 """
@@ -19,11 +20,13 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "liblora.so")
+STEP_LIB = os.path.join(HERE, "libstep.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["meta.hip", "delta.hip", "fused_dense.hip", "fused_moe.hip", "fused_moe_w2.hip", "noalloc.hip",
            "abi.cpp", "plan.cpp"]
+STEP_SOURCES = ["step_norm.hip", "step_linear.hip", "step_score.hip", "step_abi.cpp", "step_plan.cpp"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-function", "-I", os.path.join(ROOT, "include")]
@@ -45,16 +48,22 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(verbose: bool = True) -> str:
-    """Compile every source (always) and link liblora.so."""
-    os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
-    tmp = LIB + ".tmp"
+def _link(objs: list, lib: str):
+    tmp = lib + ".tmp"
     subprocess.run([HIPCC, "-shared", f"--offload-arch={ARCH}", *objs, "-o", tmp], check=True)
-    os.replace(tmp, LIB)
-    if verbose:
-        print(f"built {LIB}")
+    os.replace(tmp, lib)
+
+
+def build(verbose: bool = True) -> str:
+    """Compile every source (always) and link liblora.so and libstep.so."""
+    os.makedirs(BUILD, exist_ok=True)
+    every = SOURCES + STEP_SOURCES
+    with ThreadPoolExecutor(max_workers=len(every)) as ex:
+        objs = dict(zip(every, ex.map(_compile, every)))
+    for lib, sources in ((LIB, SOURCES), (STEP_LIB, STEP_SOURCES)):
+        _link([objs[src] for src in sources], lib)
+        if verbose:
+            print(f"built {lib}")
     return LIB
 
 

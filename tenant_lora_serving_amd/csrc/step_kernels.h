@@ -1,0 +1,88 @@
+// step_kernels.h -- host-side launch interface between step.h's entry points
+// (step_abi.cpp) and their kernels.  Internal to the library.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace st {
+
+constexpr int kMaxSlices = 8;
+constexpr int kMaxRank = 128;
+constexpr int kMaxTop = 32;
+
+struct NormArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *residual;
+    int64_t ldr;
+    const uint16_t *weight;
+    int n, h;
+    float eps;
+    uint16_t *residual_out;
+    uint16_t *y;
+    uint8_t *q;
+    float *q_scale;
+};
+hipError_t launch_rms_norm(const NormArgs &a, hipStream_t st);
+
+// A row of logits is cut into `parts` pieces, one workgroup each; the last
+// workgroup of a row to finish joins them.
+constexpr int kScoreThreads = 512;
+constexpr int kScoreLaneElems = 64;  // logits per thread of a piece at most
+constexpr int kScoreMaxParts = 64;
+// The tickets (a word a row, 0 between calls) have a place of their own, the
+// same for every shape, so that no call's records are another's tickets.
+constexpr int kScoreMaxRows = 1 << 16;
+// What a piece leaves in the workspace, in 32-bit words: maximum, two sums, a
+// count, then `top` 64-bit keys as (high, low).
+__host__ __device__ inline int score_record_words(int top) { return 4 + 2 * top; }
+struct ScorePlan {
+    int parts, part_ids;  // pieces of a row, 16-byte vectors of a piece
+    size_t ticket_bytes, total_bytes;
+};
+ScorePlan score_plan(int n, int v, int top, int fp32);
+struct ScoreArgs {
+    const void *logits;
+    int64_t ld;
+    int fp32, n, v;
+    const int32_t *tokens;
+    int top;
+    float *logprob;
+    int32_t *rank;
+    float *entropy;
+    int32_t *top_ids;
+    float *top_logprobs;
+};
+hipError_t launch_token_logprobs(const ScoreArgs &a, const ScorePlan &plan, void *ws, hipStream_t st);
+
+struct LinearArgs {
+    const uint16_t *x;
+    int64_t ldx;
+    int n, k;
+    const uint8_t *xq;
+    int64_t ldxq;
+    const float *x_scale;
+    const void *w;
+    const float *w_scale;
+    const uint16_t *a_pool;
+    const uint16_t *b_pool;
+    const float *scale;
+    int num_slots, num_slices, R;
+    int slice_off[kMaxSlices + 1];
+    const int32_t *slot;
+    uint16_t *y;
+    int64_t ldy;
+};
+// The inner sums x A_s^T are computed in k_pieces parts along k, kept apart
+// in the workspace ([piece][n][num_slices * R] fp32) and added by their
+// reader in the order of the pieces.
+struct LinearPlan {
+    int k_pieces;
+    size_t part_bytes, total_bytes;
+};
+LinearPlan linear_plan(int n, int k, int out, int num_slices, int R);
+hipError_t launch_lora_linear(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st);
+
+}  // namespace st

@@ -1,0 +1,44 @@
+// step_plan.cpp -- host-side sizing of step.h's calls: how a row of logits and
+// the inner sums of a projection are cut, and what their workspaces hold.
+#include "step_kernels.h"
+
+namespace st {
+
+namespace {
+
+size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
+long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+// At least as many pieces as keep a thread within kScoreLaneElems logits; for
+// few rows more, until the pieces number about two per CU, but not so many
+// that a thread has less than one 16-byte vector.
+ScorePlan score_plan(int n, int v, int top, int fp32) {
+    const int E = fp32 ? 4 : 8;
+    const long long ids = v / E + 2;  // whole vectors and the two ragged ends
+    const long long least = cdiv(ids, (long long)kScoreThreads * (kScoreLaneElems / E));
+    long long parts = cdiv(512, n > 0 ? n : 1);
+    if (parts > cdiv(ids, kScoreThreads)) parts = cdiv(ids, kScoreThreads);
+    if (parts > kScoreMaxParts) parts = kScoreMaxParts;
+    if (parts < least) parts = least;
+    ScorePlan p{};
+    p.part_ids = (int)cdiv(ids, parts);
+    p.parts = (int)cdiv(ids, p.part_ids);
+    if (p.parts > 1) {
+        p.ticket_bytes = (size_t)kScoreMaxRows * sizeof(int32_t);
+        p.total_bytes = p.ticket_bytes + up256((size_t)n * p.parts * score_record_words(top) * sizeof(uint32_t));
+    }
+    return p;
+}
+
+LinearPlan linear_plan(int n, int k, int out, int num_slices, int R) {
+    (void)out;
+    LinearPlan p{};
+    p.k_pieces = k >= 1024 && n <= 512 ? 4 : 1;
+    p.part_bytes = up256((size_t)p.k_pieces * n * num_slices * R * sizeof(float));
+    p.total_bytes = p.part_bytes;
+    return p;
+}
+
+}  // namespace st
