@@ -26,7 +26,8 @@ ARCH = "gfx950"
 
 SOURCES = ["meta.hip", "delta.hip", "fused_dense.hip", "fused_moe.hip", "fused_moe_w2.hip", "noalloc.hip",
            "abi.cpp", "plan.cpp"]
-STEP_SOURCES = ["step_norm.hip", "step_linear.hip", "step_score.hip", "step_abi.cpp", "step_plan.cpp"]
+STEP_SOURCES = ["step_norm.hip", "step_linear.hip", "step_linear_tiled.hip", "step_score.hip", "step_abi.cpp",
+                "step_plan.cpp"]
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wall", "-Wno-unused-function", "-I", os.path.join(ROOT, "include")]

@@ -72,7 +72,7 @@ int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const
     for (int l = num_slices + 1; l <= st::kMaxSlices; ++l) a.slice_off[l] = (int)out;
     if (int rc = check_linear(n, k, out, num_slices, max_rank)) return rc;
     if (num_slots < 1) return STEP_EINVAL;
-    if (num_slots > 8192) return STEP_EUNSUPPORTED;
+    if (num_slots > st::kMaxSlots) return STEP_EUNSUPPORTED;
     if (ldx < k || ldx % 8 != 0 || ldy < out || ldy % 8 != 0) return STEP_EINVAL;
     if (xq && (ldxq < k || ldxq % 16 != 0)) return STEP_EINVAL;
     if ((long long)n * ldx >= (1LL << 30) || (xq && (long long)n * ldxq >= (1LL << 31))) return STEP_EUNSUPPORTED;
@@ -102,7 +102,8 @@ int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const
     a.slot = slot;
     a.y = y;
     a.ldy = ldy;
-    return launched(st::launch_lora_linear(a, plan, ws, static_cast<hipStream_t>(stream)));
+    return launched((plan.tiled ? st::launch_lora_linear_tiled : st::launch_lora_linear)(
+        a, plan, ws, static_cast<hipStream_t>(stream)));
 }
 
 size_t step_token_logprobs_workspace_bytes(int32_t n, int32_t v, int32_t top) {

@@ -10,6 +10,7 @@ namespace st {
 
 constexpr int kMaxSlices = 8;
 constexpr int kMaxRank = 128;
+constexpr int kMaxSlots = 8192;
 constexpr int kMaxTop = 32;
 
 struct NormArgs {
@@ -57,6 +58,9 @@ struct ScoreArgs {
 };
 hipError_t launch_token_logprobs(const ScoreArgs &a, const ScorePlan &plan, void *ws, hipStream_t st);
 
+// Longest k at which 8-bit rows are multiplied as bf16 (step_linear.h); never tiled.
+constexpr int kExactK = 256;
+
 struct LinearArgs {
     const uint16_t *x;
     int64_t ldx;
@@ -75,14 +79,18 @@ struct LinearArgs {
     uint16_t *y;
     int64_t ldy;
 };
-// The inner sums x A_s^T are computed in k_pieces parts along k, kept apart
-// in the workspace ([piece][n][num_slices * R] fp32) and added by their
-// reader in the order of the pieces.
+// How a projection runs and what its workspace holds.  tiled: the rows' order
+// by slot and their slots in it (row_words words each), then the inner sums
+// x A_s^T as bf16 pairs.  Otherwise: the inner sums in k_pieces parts along k,
+// kept apart ([piece][n][num_slices * R] fp32) and added by their reader in
+// the order of the pieces.
 struct LinearPlan {
+    bool tiled;
     int k_pieces;
-    size_t part_bytes, total_bytes;
+    size_t row_words, total_bytes;
 };
 LinearPlan linear_plan(int n, int k, int out, int num_slices, int R);
 hipError_t launch_lora_linear(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st);
+hipError_t launch_lora_linear_tiled(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st);
 
 }  // namespace st

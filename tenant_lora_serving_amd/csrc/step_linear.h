@@ -32,9 +32,8 @@ constexpr int kLine = 128;
 // more than about 2^14 smaller (measured with three-term sums).  Over a long k
 // that averages out far below the result's rounding; over a short one it would
 // show, so there the 8-bit values, which bf16 holds exactly, go through the
-// bf16 instruction.
+// bf16 instruction (k <= kExactK).
 enum Form { kBf16, kE4m3, kE4m3AsBf16 };
-constexpr int kExactK = 256;  // longest k of kE4m3AsBf16
 
 // Eight e4m3 values as bf16 (exact).
 __device__ __forceinline__ u32x4_t widen8(uint32_t lo, uint32_t hi) {

@@ -1,0 +1,474 @@
+// step_linear_tiled.hip -- step_lora_linear for many rows, where the shared
+// product is bound by the matrix cores.
+//
+// The rows are first sorted by slot (a permutation, nothing moves), so that a
+// tile of 256 rows names few slots, and the inner sums x A_s^T are kept as
+// two bf16 terms a value.  A workgroup then computes 256 rows x 256 columns as
+// one long product over lines of 128 bytes: the lines of x and W, and after
+// them, for each slot of the tile, the line(s) of the inner sums and of B_s,
+// with zeros for the rows of other slots.  The adapters so ride in the same
+// pipeline, at 2 R / 64 lines a slot (2 of 66 at rank 64 and k 4096).
+//
+// Pipeline.  Eight waves, 2 x 4, hold 128 x 64 results each; the operands go
+// through two 64 KB buffers of LDS, filled by loads that write LDS directly.
+// A line takes four phases, one per quarter (64 x 32) of a wave's results; a
+// phase reads the fragments that are due, starts the loads of one quarter of
+// a later line, and then multiplies.  Four of the waves run half a phase
+// behind the other four (one more barrier at the start), so on every SIMD one
+// wave multiplies while the other reads.  A part of a buffer is refilled two
+// phases after its last read and used six phases after its refill was
+// started, so the wait is for loads that are 5 phases (10 loads) old.
+#include "step_linear.h"
+
+namespace st {
+
+namespace {
+
+constexpr int BM = 256, BN = 256;          // rows of x, rows of w of a tile
+constexpr int kThreads = 512;
+constexpr int kPart = 128 * kLine;         // bytes of a quarter of a buffer: 128 rows
+constexpr int kBuf = 4 * kPart;            // A0, A1, B0, B1
+
+// ---------------------------------------------------------------- sort by slot
+// One workgroup: a count per slot, their prefix sum, then each row takes the
+// next place of its slot.  Rows without an adapter come last (key S).  Which
+// row of a slot gets which place varies; no result depends on it.
+constexpr int kSortThreads = 1024;
+__global__ __launch_bounds__(kSortThreads) void sort_kernel(const int32_t *slot, int n, int S, int32_t *perm,
+                                                            int32_t *key_of) {
+    __shared__ int place[kMaxSlots + 1];
+    __shared__ int scratch[kSortThreads / kWave + 1];
+    const int tid = threadIdx.x;
+    for (int s = tid; s <= S; s += kSortThreads) place[s] = 0;
+    __syncthreads();
+    auto key_at = [&](int r) {
+        const int s = slot[r];
+        return s >= 0 && s < S ? s : S;
+    };
+    for (int r = tid; r < n; r += kSortThreads) atomicAdd(&place[key_at(r)], 1);
+    __syncthreads();
+    const int per = (S + kSortThreads) / kSortThreads, s0 = min(tid * per, S + 1), s1 = min(s0 + per, S + 1);
+    int mine = 0, total;
+    for (int s = s0; s < s1; ++s) mine += place[s];
+    int at = tl::block_excl_scan<kSortThreads>(mine, scratch, total);
+    for (int s = s0; s < s1; ++s) {
+        const int c = place[s];
+        place[s] = at;
+        at += c;
+    }
+    __syncthreads();
+    for (int r = tid; r < n; r += kSortThreads) {
+        const int key = key_at(r), p = atomicAdd(&place[key], 1);
+        perm[p] = r;
+        key_of[p] = key;
+    }
+}
+
+// ---------------------------------------------------------------- inner sums
+// scale[s] x A_s^T for 64 sorted rows and 64 of the num_slices * R rows of
+// A_s, for each slot that the rows name; written as [row][slice][R rounded
+// values, R rests] in bf16.  Four waves take every fourth line of k.
+constexpr int kInRows = 64, kInCols = 64, kInLd = kInCols + 4;
+__global__ __launch_bounds__(256) void sorted_inner_kernel(LinearArgs a, const int32_t *perm, const int32_t *key_of,
+                                                           uint16_t *xab) {
+    __shared__ float red[4 * kInRows * kInLd];
+    const int lane = tl::lane_id(), wave = tl::wave_id(), tid = threadIdx.x;
+    const int p0 = blockIdx.x * kInRows, c0 = blockIdx.y * kInCols, LR = a.num_slices * a.R;
+    const int kbytes = a.k * 2, lines = (kbytes + kLine - 1) / kLine;
+    const rsrc_t xr = tl::make_rsrc(a.x, (uint32_t)(((int64_t)(a.n - 1) * a.ldx + a.k) * 2));
+    const int my_key = p0 + lane < a.n ? key_of[p0 + lane] : a.num_slots;
+    const int my_row = p0 + lane < a.n ? perm[p0 + lane] : 0;
+    uint32_t wo[4], xo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wo[j] = c0 + 16 * j + lane % 16 < LR ? (uint32_t)((16 * j + lane % 16) * kbytes) : kOob;
+    uint64_t left = __ballot(my_key < a.num_slots);
+    while (left) {
+        const int slot = __builtin_amdgcn_readlane(my_key, __builtin_ctzll(left));
+        const uint64_t same = __ballot(my_key == slot);
+        left &= ~same;
+        const uint16_t *A = a.a_pool + ((int64_t)slot * LR + c0) * a.k;
+        const rsrc_t wr = tl::make_rsrc(A, (uint32_t)(min(LR - c0, kInCols) * kbytes));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = 16 * i + lane % 16, row = __shfl(my_row, m);
+            xo[i] = same >> m & 1 ? (uint32_t)((int64_t)row * a.ldx * 2) : kOob;
+        }
+        f32x4_t acc[4][4] = {};
+        stream_product<kBf16, 4, 4>(wr, wo, xr, xo, wave, 4, lines, kbytes, acc);
+        float *mine = red + wave * kInRows * kInLd;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4_t *>(mine + (16 * i + lane % 16) * kInLd + 16 * j + 4 * (lane / 16)) = acc[j][i];
+        __syncthreads();
+        const float scale = a.scale[slot];
+        for (int t = tid; t < kInRows * kInCols / 8; t += 256) {
+            const int m = t / (kInCols / 8), c = t % (kInCols / 8) * 8;
+            if (!(same >> m & 1) || c0 + c >= LR) continue;
+            float hi[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v += red[(w * kInRows + m) * kInLd + c + e];
+                v *= scale;
+                hi[e] = tl::bf16_round(v);
+                lo[e] = v - hi[e];
+            }
+            const int l = (c0 + c) / a.R, r = (c0 + c) % a.R;
+            uint16_t *to = xab + (((int64_t)(p0 + m) * a.num_slices + l) * 2) * a.R + r;
+            tl::st16(to, u32x4_t{tl::pack_bf16x2(hi[0], hi[1]), tl::pack_bf16x2(hi[2], hi[3]),
+                                 tl::pack_bf16x2(hi[4], hi[5]), tl::pack_bf16x2(hi[6], hi[7])});
+            tl::st16(to + a.R, u32x4_t{tl::pack_bf16x2(lo[0], lo[1]), tl::pack_bf16x2(lo[2], lo[3]),
+                                       tl::pack_bf16x2(lo[4], lo[5]), tl::pack_bf16x2(lo[6], lo[7])});
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- the tiled product
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// A buffer resource as plain words, for the asm load below.
+__device__ __forceinline__ i32x4_t words_rsrc(const void *base, uint32_t bytes) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                   __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32) & 0xffff),
+                   __builtin_amdgcn_readfirstlane((int)bytes), tl::kBufWord3};
+}
+// 16 bytes a lane from the buffer into LDS at `lds` + 16 * lane; offsets past
+// the buffer write zeros.  There is no register result, so nothing is written
+// behind the compiler's back but LDS, which "memory" covers; the waits are
+// written out below.
+__device__ __forceinline__ void load_lds(i32x4_t rsrc, uint32_t off, uint32_t more, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(rsrc), "s"(more)
+                 : "memory");
+}
+__device__ __forceinline__ void barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Which line comes next: the lines of x and W (slot < 0), or a line of a
+// slot's inner sums and B.  Wave-uniform.
+struct Cursor {
+    int line;               // lines of x and W started so far
+    int slot, slice, part;  // of the adapter line
+    int lo, hi;             // columns of the slice in this tile
+    bool done;
+};
+
+template <Form F>
+__global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int32_t *perm, const int32_t *key_of,
+                                                         const uint16_t *xab, int out) {
+    __shared__ __align__(16) char lds[2 * kBuf];
+    __shared__ int keys[BM];
+    const int lane = tl::lane_id(), tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
+
+    // Tile of this workgroup.  Each XCD takes a run of the full-height tiles
+    // in an order that walks 4 columns of tiles down the rows (32 workgroups
+    // then share 8 row and 4 column panels in its L2), then its share of the
+    // short tiles of the last rows.
+    const int m_full = a.n / BM, c_tiles = (out + BN - 1) / BN;
+    const int xcd = blockIdx.x % 8, nth = blockIdx.x / 8;
+    const int full = m_full * c_tiles, f0 = (int)((int64_t)full * xcd / 8), f1 = (int)((int64_t)full * (xcd + 1) / 8);
+    int mt, ct;
+    if (nth < f1 - f0) {
+        const int id = f0 + nth, group = id / (4 * m_full), in = id % (4 * m_full);
+        const int wide = min(4, c_tiles - 4 * group);
+        mt = in / wide;
+        ct = 4 * group + in % wide;
+    } else {
+        const int shorts = a.n % BM ? c_tiles : 0;
+        const int s0 = shorts * xcd / 8, s1 = shorts * (xcd + 1) / 8;
+        mt = m_full;
+        ct = s0 + nth - (f1 - f0);
+        if (ct >= s1) return;
+    }
+    const int m0 = mt * BM, c0 = ct * BN, rows = min(a.n - m0, BM), cols = min(out - c0, BN);
+
+    if (tid < BM) keys[tid] = tid < rows ? key_of[m0 + tid] : a.num_slots;
+    __syncthreads();
+
+    static_assert(F != kE4m3AsBf16, "short k is not tiled");
+    constexpr int esz = F == kBf16 ? 2 : 1;
+    const int kbytes = a.k * esz, lines = (kbytes + kLine - 1) / kLine;
+    const int64_t ldx = F == kBf16 ? a.ldx * 2 : a.ldxq;
+    const void *xb = F == kBf16 ? (const void *)a.x : (const void *)a.xq;
+    const i32x4_t xr = words_rsrc(xb, (uint32_t)((int64_t)(a.n - 1) * ldx + kbytes));
+    const i32x4_t wr = words_rsrc((const char *)a.w + (int64_t)c0 * kbytes, (uint32_t)(cols * kbytes));
+    const int xab_ld = a.num_slices * 2 * a.R * 2;  // bytes a row of the inner sums
+    const i32x4_t ar = words_rsrc((const char *)xab + (int64_t)m0 * xab_ld, (uint32_t)(rows * xab_ld));
+
+    // A quarter of a buffer is loaded by 16 wave loads of 8 rows, two a wave.
+    // LDS slot s (16 bytes) of row r holds chunk s ^ (r % 8): the reads of 16
+    // rows at one chunk then fall on different banks.
+    const int l8 = lane / 8, chunk = (lane % 8) ^ l8;
+    int ra[2], rb[2];  // tile rows of the lane's loads in A0 and B0; A1: + 64, B1: + 32
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = wave * 2 + u;
+        ra[u] = (i / 8) * 128 + (i % 8) * 8 + l8;
+        rb[u] = (i / 4) * 64 + (i % 4) * 8 + l8;
+    }
+    // Byte offsets of the lane's chunk in line 0 of its rows: A0, A0, A1, A1
+    // and B0, B0, B1, B1.  Absent rows read the first one's: their products
+    // reach no result that is stored.
+    uint32_t xo[4], wo[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int r = ra[u & 1] + 64 * (u / 2), c = rb[u & 1] + 32 * (u / 2);
+        xo[u] = (uint32_t)((int64_t)perm[m0 + (r < rows ? r : 0)] * ldx) + chunk * 16;
+        wo[u] = (uint32_t)((c < cols ? c : 0) * kbytes) + chunk * 16;
+    }
+
+    // ---- the adapter lines of this tile
+    const int parts = (2 * a.R + 63) / 64, chunks = a.R / 8;
+    int first_slice = 0, end_slice = a.num_slices;
+    while (a.slice_off[first_slice + 1] <= c0) ++first_slice;
+    while (end_slice > first_slice + 1 && a.slice_off[end_slice - 1] >= c0 + cols) --end_slice;
+    // rows with a key <= k; keys ascend, so this is the next slot's first row
+    auto rows_upto = [&](int k) {
+        int c = 0;
+#pragma unroll
+        for (int u = 0; u < BM / kWave; ++u) c += __popcll(__ballot(keys[u * kWave + lane] <= k));
+        return c;
+    };
+    auto slot_at = [&](int p) { return p < BM ? __builtin_amdgcn_readfirstlane(keys[p]) : a.num_slots; };
+    int distinct = 0;
+    for (int s = slot_at(0); s < a.num_slots; s = slot_at(rows_upto(s))) ++distinct;
+    const int total = lines + distinct * (end_slice - first_slice) * parts;
+
+    Cursor cur{0, -1, first_slice, 0, 0, 0, false};
+    i32x4_t br = wr;
+    auto enter_slice = [&](int l) {
+        cur.slice = l;
+        cur.lo = a.slice_off[l] - c0;
+        cur.hi = a.slice_off[l + 1] - c0;
+    };
+    auto enter_slot = [&](int s) {
+        cur.slot = s;
+        cur.done = s >= a.num_slots;
+        enter_slice(first_slice);
+        if (!cur.done)
+            br = words_rsrc(a.b_pool + ((int64_t)s * out + c0) * a.R, (uint32_t)((int64_t)cols * a.R * 2));
+    };
+    auto advance = [&]() {
+        if (cur.line < lines) {
+            if (++cur.line == lines) enter_slot(slot_at(0));
+        } else if (!cur.done) {
+            if (++cur.part == parts) {
+                cur.part = 0;
+                if (cur.slice + 1 < end_slice) enter_slice(cur.slice + 1);
+                else enter_slot(slot_at(rows_upto(cur.slot)));
+            }
+        }
+    };
+    const uint32_t lds0 =
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds + __builtin_amdgcn_readfirstlane(wave * 2048);
+    // Starts the loads of part P (0 A0, 1 A1, 2 B0, 3 B1) of a line into buffer b: a whole line of x and W, ...
+    auto start_whole = [&](int b, int line, auto part_of) {
+        constexpr int P = decltype(part_of)::value, H = P & 1;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            load_lds(P < 2 ? xr : wr, (P < 2 ? xo : wo)[2 * H + u], line * kLine, lds0 + b * kBuf + P * kPart + u * 1024);
+    };
+    // ... or the cursor's line, whichever it is.
+    auto start_any = [&](int b, auto part_of) {
+        constexpr int P = decltype(part_of)::value, H = P & 1;
+        uint32_t off[2];
+        i32x4_t rsrc;
+        if (cur.line < lines) {
+            const int at = cur.line * kLine;
+            rsrc = P < 2 ? xr : wr;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) off[u] = at + chunk * 16 < kbytes ? (P < 2 ? xo : wo)[2 * H + u] + at : kOob;
+        } else {
+            const int q = cur.part * 8 + chunk;  // of R/8 chunks of rounded values, then R/8 of rests
+            const bool in = (int)!cur.done & (int)(q < 2 * chunks);
+            rsrc = P < 2 ? ar : br;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if constexpr (P < 2) {
+                    const int r = ra[u] + 64 * H;
+                    off[u] = (int)in & (int)(keys[r] == cur.slot) ? (uint32_t)(r * xab_ld + cur.slice * 4 * a.R + q * 16)
+                                                                  : kOob;
+                } else {
+                    const int c = rb[u] + 32 * H;
+                    off[u] = (int)in & (int)(c >= cur.lo) & (int)(c < cur.hi)
+                                 ? (uint32_t)(c * a.R * 2 + (q >= chunks ? q - chunks : q) * 16)
+                                 : kOob;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) load_lds(rsrc, off[u], 0, lds0 + b * kBuf + P * kPart + u * 1024);
+    };
+    using P0 = std::integral_constant<int, 0>;
+    using P1 = std::integral_constant<int, 1>;
+    using P2 = std::integral_constant<int, 2>;
+    using P3 = std::integral_constant<int, 3>;
+
+    // ---- fragments
+    const int wm = wave / 4, wn = wave % 4;
+    const int rd = (lane % 16) * kLine + (((lane / 16) ^ (lane & 7)) * 16);
+    const char *ra_base = lds + wm * 64 * kLine, *rb_base = lds + 2 * kPart + wn * 32 * kLine;
+    Line fa[2][4], fb[2][2];
+    f32x4_t acc[4][8] = {};  // [column tile][row tile]
+    auto read_a = [&](int b, int h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const char *p = ra_base + b * kBuf + h * kPart + i * 16 * kLine;
+            fa[h][i] = Line{tl::ld16(p + rd), tl::ld16(p + (rd ^ 64))};
+        }
+    };
+    auto read_b = [&](int b, int h) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const char *p = rb_base + b * kBuf + h * kPart + j * 16 * kLine;
+            fb[h][j] = Line{tl::ld16(p + rd), tl::ld16(p + (rd ^ 64))};
+        }
+    };
+    const int live = rows - wm * 128;  // rows of this wave
+    auto multiply = [&](auto form, int ha, int hb) {
+        barrier();
+        if (live > ha * 64) {
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[2 * hb + j][4 * ha + i] =
+                        mma_line<decltype(form)::value>(fb[hb][j], fa[ha][i], acc[2 * hb + j][4 * ha + i]);
+            __builtin_amdgcn_s_setprio(0);
+        }
+        barrier();
+    };
+
+    // ---- fill: line 0 whole, line 1 but its A1 (the first phase starts that).
+    // In steady state a phase waits with the 10 newest loads still out.
+    start_any(0, P0{});
+    start_any(0, P2{});
+    start_any(0, P3{});
+    start_any(0, P1{});
+    advance();
+    start_any(1, P0{});
+    start_any(1, P2{});
+    start_any(1, P3{});
+    wait_loads<12>();  // A0 of line 0 is there
+    barrier();
+    if (wave >= 4) barrier();  // half a phase behind
+    read_a(0, 0);
+    wait_loads<10>();  // and B0
+    barrier();
+    barrier();
+    // The line t in buffer b.  whole: lines t + 1 and t + 2 are whole lines of x and W.
+    auto line_step = [&](auto form, auto whole, int t, int b) {
+        constexpr bool W = decltype(whole)::value;
+        // phase 1: B0; starts A1 of the next line
+        read_b(b, 0);
+        if constexpr (W) start_whole(b ^ 1, t + 1, P1{});
+        else start_any(b ^ 1, P1{});
+        wait_loads<10>();
+        multiply(form, 0, 0);
+        // phase 2: B1; starts A0 of the line after it
+        if constexpr (!W) advance();
+        read_b(b, 1);
+        if constexpr (W) start_whole(b, t + 2, P0{});
+        else start_any(b, P0{});
+        wait_loads<10>();
+        multiply(form, 0, 1);
+        // phase 3: A1
+        read_a(b, 1);
+        if constexpr (W) start_whole(b, t + 2, P2{});
+        else start_any(b, P2{});
+        wait_loads<10>();
+        multiply(form, 1, 1);
+        // phase 4: A0 of the next line
+        read_a(b ^ 1, 0);
+        if constexpr (W) start_whole(b, t + 2, P3{});
+        else start_any(b, P3{});
+        wait_loads<10>();
+        multiply(form, 1, 0);
+    };
+    using Main = std::integral_constant<Form, F>;
+    using Extra = std::integral_constant<Form, kBf16>;
+    int t = 0;
+    for (; t + 3 < kbytes / kLine; t += 2) {
+        line_step(Main{}, std::true_type{}, t, 0);
+        line_step(Main{}, std::true_type{}, t + 1, 1);
+    }
+    if (t > 0) cur.line = t + 1;  // (line t + 1 is started but for its A1)
+#pragma unroll 1
+    for (; t < lines; ++t) line_step(Main{}, std::false_type{}, t, t & 1);
+    if constexpr (F != kBf16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int m = wm * 128 + 16 * i + lane % 16;
+            const float xs = m < rows ? a.x_scale[perm[m0 + m]] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][i][e] *= xs;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = wn * 64 + 16 * j + 4 * (lane / 16) + e;
+                const float ws = c < cols ? a.w_scale[c0 + c] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[j][i][e] *= ws;
+            }
+    }
+#pragma unroll 1
+    for (; t < total; ++t) line_step(Extra{}, std::false_type{}, t, t & 1);
+    if (wave < 4) barrier();
+    wait_loads<0>();  // nothing may still write LDS when the workgroup ends
+
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int m = wm * 128 + 16 * i + lane % 16;
+        if (m >= rows) continue;
+        uint16_t *y = a.y + (int64_t)perm[m0 + m] * a.ldy + c0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = wn * 64 + 16 * j + 4 * (lane / 16);
+            if (c < cols)
+                *reinterpret_cast<uint2 *>(y + c) = make_uint2(tl::pack_bf16x2(acc[j][i][0], acc[j][i][1]),
+                                                               tl::pack_bf16x2(acc[j][i][2], acc[j][i][3]));
+        }
+    }
+}
+
+template <Form F>
+void go(const LinearArgs &a, const int32_t *perm, const int32_t *key_of, const uint16_t *xab, int out,
+        hipStream_t st) {
+    const int c_tiles = (out + BN - 1) / BN, full = a.n / BM * c_tiles, shorts = a.n % BM ? c_tiles : 0;
+    tiled_kernel<F><<<dim3(8 * ((full + 7) / 8 + (shorts + 7) / 8)), kThreads, 0, st>>>(a, perm, key_of, xab, out);
+}
+
+}  // namespace
+
+hipError_t launch_lora_linear_tiled(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st) {
+    int32_t *perm = static_cast<int32_t *>(ws), *key_of = perm + plan.row_words;
+    uint16_t *xab = reinterpret_cast<uint16_t *>(key_of + plan.row_words);
+    const int out = a.slice_off[a.num_slices];
+    sort_kernel<<<1, kSortThreads, 0, st>>>(a.slot, a.n, a.num_slots, perm, key_of);
+    sorted_inner_kernel<<<dim3((a.n + kInRows - 1) / kInRows, (a.num_slices * a.R + kInCols - 1) / kInCols), 256, 0,
+                          st>>>(a, perm, key_of, xab);
+    if (a.xq) go<kE4m3>(a, perm, key_of, xab, out, st);
+    else go<kBf16>(a, perm, key_of, xab, out, st);
+    return hipGetLastError();
+}
+
+}  // namespace st
