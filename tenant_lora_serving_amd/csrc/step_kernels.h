@@ -81,12 +81,9 @@ struct LinearArgs {
 };
 // How a projection runs and what its workspace holds.  tiled: the rows' order
 // by slot and their slots in it (row_words words each), then the inner sums
-// x A_s^T as bf16 pairs.  Otherwise: the inner sums in k_pieces parts along k,
-// kept apart ([piece][n][num_slices * R] fp32) and added by their reader in
-// the order of the pieces.
+// of the rows in that order; otherwise the inner sums alone.
 struct LinearPlan {
     bool tiled;
-    int k_pieces;
     size_t row_words, total_bytes;
 };
 LinearPlan linear_plan(int n, int k, int out, int num_slices, int R);

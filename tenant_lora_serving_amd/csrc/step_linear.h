@@ -67,39 +67,152 @@ __device__ __forceinline__ f32x4_t mma_line(const Line &w, const Line &x, f32x4_
     }
 }
 
+// ---------------------------------------------------------------- loads into LDS
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// A buffer resource as plain words, for the asm load below.
+__device__ __forceinline__ i32x4_t words_rsrc(const void *base, uint32_t bytes) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                   __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32) & 0xffff),
+                   __builtin_amdgcn_readfirstlane((int)bytes), tl::kBufWord3};
+}
+// 16 bytes a lane from the buffer into LDS at `lds` + 16 * lane; offsets past
+// the buffer write zeros.  There is no register result, so nothing is written
+// behind the compiler's back but LDS, which "memory" covers; the waits are
+// written out below.
+__device__ __forceinline__ void load_lds(i32x4_t rsrc, uint32_t off, uint32_t more, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(rsrc), "s"(more)
+                 : "memory");
+}
+__device__ __forceinline__ void barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+// At most N of the wave's loads are still out.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const char *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
+
+// A wave's own ring of lines in LDS: a slot holds one line of NT tiles of w
+// and MT tiles of x, 16 rows each.  Chunk c (16 bytes) of row r lies at place
+// c ^ (r % 8) of the row, so that 16 rows' reads of one chunk fall on
+// different banks.  A load instruction fills 8 rows, whole lines of memory.
+template <int NT, int MT, int SLOTS>
+struct LineRing {
+    static constexpr int kSlot = (NT + MT) * 16 * kLine, kBytes = SLOTS * kSlot;
+    static constexpr int kW = 2 * NT, kX = 2 * MT;  // load instructions of a line
+    // The row that the lane's u-th load of w (or of x) belongs to.
+    static __device__ __forceinline__ int row(int u) { return 8 * u + tl::lane_id() / 8; }
+};
+
 // acc[j][i] += W tile j (16 rows) * X tile i (16 rows)^T over the lines
-// first, first + stride, ... of `lines`, both operands loaded in matrix-core
-// layout from memory, one line ahead of its use.  wo / xo: byte offset of the
-// lane's row (kOob for an absent row); a chunk past `kbytes` reads as zero on
+// first, first + stride, ... of `lines`, by one wave on its own: lines come
+// through its ring SLOTS - 1 ahead of their use, and a slot is refilled as
+// soon as its fragments are in registers, so there is no barrier and the
+// loads never pause for the products.  (Loads straight to registers in
+// matrix-core layout take 16 rows x 64 bytes an instruction and ran at a
+// third of this rate: a CU's outstanding lines bound them.)
+// wo / xo: byte offset of the row of each of the lane's loads (kOob for an
+// absent row); chunks past `kbytes` and lines past the last read as zero on
 // both sides.  (An absent row's chunk past the end wraps to some offset in
 // range: what it reads reaches only the absent row's products.)
-template <Form F, int NT, int MT>
-__device__ __forceinline__ void stream_product(rsrc_t wr, const uint32_t *wo, rsrc_t xr, const uint32_t *xo, int first,
-                                               int stride, int lines, int kbytes, f32x4_t (&acc)[NT][MT]) {
-    const int g = (tl::lane_id() / 16) * 16;
-    Line w[2][NT], x[2][MT];
-    auto fetch = [&](int b, int s) {
-        const int at = s * kLine + g;
-        const uint32_t o0 = at < kbytes ? (uint32_t)at : kOob, o1 = at + 64 < kbytes ? (uint32_t)at + 64 : kOob;
+template <Form F, int NT, int MT, int SLOTS>
+__device__ __forceinline__ void ring_product(i32x4_t wr, const uint32_t *wo, i32x4_t xr, const uint32_t *xo, char *ring,
+                                             int first, int stride, int lines, int kbytes, f32x4_t (&acc)[NT][MT]) {
+    using Ring = LineRing<NT, MT, SLOTS>;
+    static_assert((SLOTS - 1) * (Ring::kW + Ring::kX) < 64, "the wait counts to 63");
+    const int lane = tl::lane_id();
+    const int chunk = ((lane & 7) ^ (lane / 8)) * 16;
+    const uint32_t base = lds_address(ring);
+    const int rd = (lane % 16) * kLine + (((lane / 16) ^ (lane & 7)) * 16);
+    auto start = [&](int slot, int line) {
+        const int at = line * kLine + chunk;
+        const uint32_t o = at < kbytes ? (uint32_t)at : kOob;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) w[b][j] = Line{tl::buf_ld16(wr, wo[j] + o0), tl::buf_ld16(wr, wo[j] + o1)};
+        for (int u = 0; u < Ring::kW; ++u) load_lds(wr, wo[u] + o, 0, base + slot * Ring::kSlot + u * 1024);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) x[b][i] = Line{tl::buf_ld16(xr, xo[i] + o0), tl::buf_ld16(xr, xo[i] + o1)};
+        for (int u = 0; u < Ring::kX; ++u) load_lds(xr, xo[u] + o, 0, base + slot * Ring::kSlot + (Ring::kW + u) * 1024);
     };
-    auto use = [&](int b) {
+#pragma unroll
+    for (int d = 0; d < SLOTS; ++d) start(d, first + d * stride);
+#pragma unroll 1
+    for (int s = first; s < lines; s += SLOTS * stride) {
+#pragma unroll
+        for (int d = 0; d < SLOTS; ++d) {
+            wait_loads<(SLOTS - 1) * (Ring::kW + Ring::kX)>();
+            const char *p = ring + d * Ring::kSlot;
+            Line w[NT], x[MT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                w[j] = Line{tl::ld16(p + j * 2048 + rd), tl::ld16(p + j * 2048 + (rd ^ 64))};
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                x[i] = Line{tl::ld16(p + (NT + i) * 2048 + rd), tl::ld16(p + (NT + i) * 2048 + (rd ^ 64))};
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before it is refilled
+            __builtin_amdgcn_sched_barrier(0);
+            start(d, s + (d + SLOTS) * stride);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) acc[j][i] = mma_line<F>(w[j], x[i], acc[j][i]);
+        }
+    }
+    wait_loads<0>();  // (lines past the end still write zeros to the ring)
+}
+
+// Partial tiles of several waves side by side in shared memory, [wave][x row]
+// [w row], 4 floats between rows against bank conflicts.
+template <int NT, int MT>
+struct Partials {
+    static constexpr int kRows = 16 * MT, kCols = 16 * NT, kLd = kCols + 4, kFloats = kRows * kLd;
+    static __device__ __forceinline__ void put(float *red, int wave, const f32x4_t (&acc)[NT][MT]) {
+        const int lane = tl::lane_id();
+        float *mine = red + wave * kFloats + (lane % 16) * kLd + 4 * (lane / 16);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int i = 0; i < MT; ++i) acc[j][i] = mma_line<F>(w[b][j], x[b][i], acc[j][i]);
-    };
-    if (first >= lines) return;
-    fetch(0, first);
-    for (int s = first; s < lines; s += 2 * stride) {
-        if (s + stride < lines) fetch(1, s + stride);
-        use(0);
-        if (s + 2 * stride < lines) fetch(0, s + 2 * stride);
-        if (s + stride < lines) use(1);
+            for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4_t *>(mine + 16 * i * kLd + 16 * j) = acc[j][i];
     }
+    // Eight columns of a row, the waves added in their order.
+    template <int WAVES>
+    static __device__ __forceinline__ void sum8(const float *red, int row, int col, float *v) {
+        f32x4_t lo = {}, hi = {};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float *p = red + w * kFloats + row * kLd + col;
+            lo += *reinterpret_cast<const f32x4_t *>(p);
+            hi += *reinterpret_cast<const f32x4_t *>(p + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+    }
+};
+
+__device__ __forceinline__ u32x4_t pack8(const float *v) {
+    return u32x4_t{tl::pack_bf16x2(v[0], v[1]), tl::pack_bf16x2(v[2], v[3]), tl::pack_bf16x2(v[4], v[5]),
+                   tl::pack_bf16x2(v[6], v[7])};
+}
+
+// The inner sums scale[s] x A_s^T travel as two bf16 terms a value (16 bits of
+// mantissa; one term alone would add an error of the size of the result's own
+// rounding): [row][slice][R rounded values, then R rests].
+__device__ __forceinline__ void put_inner8(uint16_t *xab, int64_t row, int c, int num_slices, int R, const float *v) {
+    float rest[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rest[e] = v[e] - tl::bf16_round(v[e]);
+    uint16_t *to = xab + ((row * num_slices + c / R) * 2) * R + c % R;
+    tl::st16(to, pack8(v));
+    tl::st16(to + R, pack8(rest));
 }
 
 }  // namespace st

@@ -65,98 +65,60 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const int32_t *slot,
 }
 
 // ---------------------------------------------------------------- inner sums
-// scale[s] x A_s^T for 64 sorted rows and 64 of the num_slices * R rows of
+// scale[s] x A_s^T for 32 sorted rows and 64 of the num_slices * R rows of
 // A_s, for each slot that the rows name; written as [row][slice][R rounded
 // values, R rests] in bf16.  Four waves take every fourth line of k.
-constexpr int kInRows = 64, kInCols = 64, kInLd = kInCols + 4;
+constexpr int kInMT = 2, kInNT = 4, kInSlots = 2, kInRows = 16 * kInMT, kInCols = 16 * kInNT;
 __global__ __launch_bounds__(256) void sorted_inner_kernel(LinearArgs a, const int32_t *perm, const int32_t *key_of,
                                                            uint16_t *xab) {
-    __shared__ float red[4 * kInRows * kInLd];
-    const int lane = tl::lane_id(), wave = tl::wave_id(), tid = threadIdx.x;
+    using Part = Partials<kInNT, kInMT>;
+    using Ring = LineRing<kInNT, kInMT, kInSlots>;
+    __shared__ __align__(16) char shared[4 * Ring::kBytes > 4 * Part::kFloats * 4 ? 4 * Ring::kBytes : 4 * Part::kFloats * 4];
+    float *red = reinterpret_cast<float *>(shared);
+    const int lane = tl::lane_id(), tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
+    char *ring = shared + wave * Ring::kBytes;
     const int p0 = blockIdx.x * kInRows, c0 = blockIdx.y * kInCols, LR = a.num_slices * a.R;
     const int kbytes = a.k * 2, lines = (kbytes + kLine - 1) / kLine;
-    const rsrc_t xr = tl::make_rsrc(a.x, (uint32_t)(((int64_t)(a.n - 1) * a.ldx + a.k) * 2));
-    const int my_key = p0 + lane < a.n ? key_of[p0 + lane] : a.num_slots;
-    const int my_row = p0 + lane < a.n ? perm[p0 + lane] : 0;
-    uint32_t wo[4], xo[4];
+    const i32x4_t xr = words_rsrc(a.x, (uint32_t)(((int64_t)(a.n - 1) * a.ldx + a.k) * 2));
+    const bool here = lane < kInRows && p0 + lane < a.n;
+    const int my_key = here ? key_of[p0 + lane] : a.num_slots;
+    const int my_row = here ? perm[p0 + lane] : 0;
+    uint32_t wo[Ring::kW], xo[Ring::kX];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) wo[j] = c0 + 16 * j + lane % 16 < LR ? (uint32_t)((16 * j + lane % 16) * kbytes) : kOob;
+    for (int u = 0; u < Ring::kW; ++u)
+        wo[u] = c0 + Ring::row(u) < LR ? (uint32_t)(Ring::row(u) * kbytes) : kOob;
     uint64_t left = __ballot(my_key < a.num_slots);
     while (left) {
         const int slot = __builtin_amdgcn_readlane(my_key, __builtin_ctzll(left));
         const uint64_t same = __ballot(my_key == slot);
         left &= ~same;
         const uint16_t *A = a.a_pool + ((int64_t)slot * LR + c0) * a.k;
-        const rsrc_t wr = tl::make_rsrc(A, (uint32_t)(min(LR - c0, kInCols) * kbytes));
+        const i32x4_t wr = words_rsrc(A, (uint32_t)(min(LR - c0, kInCols) * kbytes));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = 16 * i + lane % 16, row = __shfl(my_row, m);
-            xo[i] = same >> m & 1 ? (uint32_t)((int64_t)row * a.ldx * 2) : kOob;
+        for (int u = 0; u < Ring::kX; ++u) {
+            const int m = Ring::row(u), row = __shfl(my_row, m);
+            xo[u] = same >> m & 1 ? (uint32_t)((int64_t)row * a.ldx * 2) : kOob;
         }
-        f32x4_t acc[4][4] = {};
-        stream_product<kBf16, 4, 4>(wr, wo, xr, xo, wave, 4, lines, kbytes, acc);
-        float *mine = red + wave * kInRows * kInLd;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4_t *>(mine + (16 * i + lane % 16) * kInLd + 16 * j + 4 * (lane / 16)) = acc[j][i];
+        f32x4_t acc[kInNT][kInMT] = {};
+        ring_product<kBf16, kInNT, kInMT, kInSlots>(wr, wo, xr, xo, ring, wave, 4, lines, kbytes, acc);
+        __syncthreads();  // (the partial sums lie over the rings)
+        Part::put(red, wave, acc);
         __syncthreads();
         const float scale = a.scale[slot];
         for (int t = tid; t < kInRows * kInCols / 8; t += 256) {
             const int m = t / (kInCols / 8), c = t % (kInCols / 8) * 8;
             if (!(same >> m & 1) || c0 + c >= LR) continue;
-            float hi[8], lo[8];
+            float v[8];
+            Part::sum8<4>(red, m, c, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float v = 0.0f;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) v += red[(w * kInRows + m) * kInLd + c + e];
-                v *= scale;
-                hi[e] = tl::bf16_round(v);
-                lo[e] = v - hi[e];
-            }
-            const int l = (c0 + c) / a.R, r = (c0 + c) % a.R;
-            uint16_t *to = xab + (((int64_t)(p0 + m) * a.num_slices + l) * 2) * a.R + r;
-            tl::st16(to, u32x4_t{tl::pack_bf16x2(hi[0], hi[1]), tl::pack_bf16x2(hi[2], hi[3]),
-                                 tl::pack_bf16x2(hi[4], hi[5]), tl::pack_bf16x2(hi[6], hi[7])});
-            tl::st16(to + a.R, u32x4_t{tl::pack_bf16x2(lo[0], lo[1]), tl::pack_bf16x2(lo[2], lo[3]),
-                                       tl::pack_bf16x2(lo[4], lo[5]), tl::pack_bf16x2(lo[6], lo[7])});
+            for (int e = 0; e < 8; ++e) v[e] *= scale;
+            put_inner8(xab, p0 + m, c0 + c, a.num_slices, a.R, v);
         }
         __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------- the tiled product
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-
-// A buffer resource as plain words, for the asm load below.
-__device__ __forceinline__ i32x4_t words_rsrc(const void *base, uint32_t bytes) {
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
-                   __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32) & 0xffff),
-                   __builtin_amdgcn_readfirstlane((int)bytes), tl::kBufWord3};
-}
-// 16 bytes a lane from the buffer into LDS at `lds` + 16 * lane; offsets past
-// the buffer write zeros.  There is no register result, so nothing is written
-// behind the compiler's back but LDS, which "memory" covers; the waits are
-// written out below.
-__device__ __forceinline__ void load_lds(i32x4_t rsrc, uint32_t off, uint32_t more, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(lds), "v"(off), "s"(rsrc), "s"(more)
-                 : "memory");
-}
-__device__ __forceinline__ void barrier() {
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_barrier" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-}
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // Which line comes next: the lines of x and W (slot < 0), or a line of a
 // slot's inner sums and B.  Wave-uniform.
 struct Cursor {
@@ -274,7 +236,7 @@ __global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int
         }
     };
     const uint32_t lds0 =
-        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds + __builtin_amdgcn_readfirstlane(wave * 2048);
+        lds_address(lds) + wave * 2048;
     // Starts the loads of part P (0 A0, 1 A1, 2 B0, 3 B1) of a line into buffer b: a whole line of x and W, ...
     auto start_whole = [&](int b, int line, auto part_of) {
         constexpr int P = decltype(part_of)::value, H = P & 1;

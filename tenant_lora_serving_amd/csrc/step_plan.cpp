@@ -36,15 +36,9 @@ LinearPlan linear_plan(int n, int k, int out, int num_slices, int R) {
     LinearPlan p{};
     p.tiled = n > 1024 && k > kExactK;
     (void)out;
-    const size_t inner = (size_t)n * num_slices * R * sizeof(float);
-    if (p.tiled) {
-        p.k_pieces = 1;
-        p.row_words = up256((size_t)n * sizeof(int32_t)) / sizeof(int32_t);
-        p.total_bytes = 2 * p.row_words * sizeof(int32_t) + up256(inner);
-    } else {
-        p.k_pieces = k >= 1024 && n <= 512 ? 4 : 1;
-        p.total_bytes = up256(p.k_pieces * inner);
-    }
+    const size_t inner = (size_t)n * num_slices * R * 2 * sizeof(uint16_t);
+    if (p.tiled) p.row_words = up256((size_t)n * sizeof(int32_t)) / sizeof(int32_t);
+    p.total_bytes = 2 * p.row_words * sizeof(int32_t) + up256(inner);
     return p;
 }
 
