@@ -12,12 +12,13 @@ library, and raises LoraError on a non-zero status.  There is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional
 
 import torch
 
-from .lora import LoraError, _c_f, _c_i32, _c_i64, _c_p, _c_sz, _dev, _stream
+from .lora import LoraError, _c_f, _c_i32, _c_i64, _c_p, _c_sz, _dev
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libstep.so")
@@ -61,6 +62,15 @@ def _check(fn: str, status: int):
         raise LoraError(fn, status, lib().step_status_string(status).decode())
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # what torch.cuda.current_stream() wraps, at a fortieth of its time
+
+
+def _on(stream, fn, args, kw):
+    """The call on another stream: what it allocates belongs to that stream."""
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
+
+
 def _rows(t: torch.Tensor, name: str, *dtypes) -> tuple:
     """A 2-D tensor of rows with unit column stride: (pointer, row stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -73,9 +83,30 @@ def _rows(t: torch.Tensor, name: str, *dtypes) -> tuple:
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
 
 
+def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """A contiguous tensor of this type and shape on device `dev`: its pointer."""
+    p = _dev(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    return p
+
+
 def _same(name: str, got, want):
     if tuple(got) != tuple(want):
         raise ValueError(f"{name} must have shape {tuple(want)}, got {tuple(got)}")
+
+
+def _device(x: torch.Tensor, *rest) -> int:
+    """The device of the call: the current one, which holds every tensor."""
+    dev = x.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on device {dev}, which is not the current one")
+    return dev
 
 
 # ---------------------------------------------------------------- norm
@@ -93,29 +124,29 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, *, residu
     the unrounded s.  bf16: return y; quant: return its e4m3 copy with one
     scale a row.  residual_out: where to put the rounded s (it may be
     `residual` itself, which is then updated in place)."""
+    if stream is not None:
+        return _on(stream, rms_norm, (x, weight, eps), dict(residual=residual, bf16=bf16, quant=quant,
+                                                            residual_out=residual_out))
     xp, ldx = _rows(x, "x", torch.bfloat16)
     n, h = x.shape
-    wp = _dev(weight, "weight", torch.bfloat16)
-    _same("weight", weight.shape, (h,))
-    dev = x.device
+    dev = _device(x, residual)
+    wp = _arg(weight, "weight", torch.bfloat16, (h,), dev)
     rp, ldr, sp = None, 0, None
     if residual is not None:
         rp, ldr = _rows(residual, "residual", torch.bfloat16)
         _same("residual", residual.shape, (n, h))
         if residual_out is None:
-            residual_out = torch.empty((n, h), dtype=torch.bfloat16, device=dev)
-        else:
-            _same("residual_out", residual_out.shape, (n, h))
-        sp = _dev(residual_out, "residual_out", torch.bfloat16)
+            residual_out = x.new_empty((n, h))
+        sp = _arg(residual_out, "residual_out", torch.bfloat16, (n, h), dev)
         if sp == rp:
             ldr = h if n <= 1 else ldr
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    y = torch.empty((n, h), dtype=torch.bfloat16, device=dev) if bf16 else None
-    q = torch.empty((n, h), dtype=torch.float8_e4m3fn, device=dev) if quant else None
-    q_scale = torch.empty((n,), dtype=torch.float32, device=dev) if quant else None
+    y = x.new_empty((n, h)) if bf16 else None
+    q = x.new_empty((n, h), dtype=torch.float8_e4m3fn) if quant else None
+    q_scale = x.new_empty(n, dtype=torch.float32) if quant else None
     st = lib().step_rms_norm(xp, ldx, rp, ldr, wp, n, h, eps, sp, y.data_ptr() if bf16 else None,
-                             q.data_ptr() if quant else None, q_scale.data_ptr() if quant else None, _stream(stream))
+                             q.data_ptr() if quant else None, q_scale.data_ptr() if quant else None, _raw_stream(dev))
     if st:
         _check("step_rms_norm", st)
     return NormResult(y, residual_out, q, q_scale)
@@ -127,6 +158,12 @@ def linear_workspace(n: int, k: int, out: int, num_slices: int, max_rank: int, d
     return torch.zeros(max(b, 16), dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=256)
+def _slice_array(sizes: tuple) -> tuple:
+    """The widths as the library takes them, and their sum."""
+    return (_c_i32 * len(sizes))(*sizes), sum(sizes)
+
+
 def lora_linear(x: torch.Tensor, w: torch.Tensor, a_pool: torch.Tensor, b_pool: torch.Tensor, scale: torch.Tensor,
                 slice_sizes, slot: torch.Tensor, *, xq: Optional[torch.Tensor] = None,
                 x_scale: Optional[torch.Tensor] = None, w_scale: Optional[torch.Tensor] = None,
@@ -136,18 +173,20 @@ def lora_linear(x: torch.Tensor, w: torch.Tensor, a_pool: torch.Tensor, b_pool: 
     w [N, k] bf16; or, with xq [n, k] (float8_e4m3fn), x_scale [n] and w_scale
     [N], w in float8_e4m3fn and the first term from the 8-bit rows.
     a_pool [S, L, R, k], b_pool [S, N, R], slice_sizes L widths that add up to N."""
+    if stream is not None:
+        return _on(stream, lora_linear, (x, w, a_pool, b_pool, scale, slice_sizes, slot),
+                   dict(xq=xq, x_scale=x_scale, w_scale=w_scale, out=out, ws=ws))
     if a_pool.dim() != 4 or b_pool.dim() != 3 or w.dim() != 2:
         raise ValueError("a_pool must be [S, L, R, k], b_pool [S, N, R] and w [N, k]")
     S, L, R, k = a_pool.shape
     N = w.shape[0]
     n = x.shape[0]
     xp, ldx = _rows(x, "x", torch.bfloat16)
-    _same("x", x.shape, (n, k))
-    _same("w", w.shape, (N, k))
-    _same("b_pool", b_pool.shape, (S, N, R))
-    _same("scale", scale.shape, (S,))
-    _same("slot", slot.shape, (n,))
-    if len(slice_sizes) != L or sum(slice_sizes) != N:
+    if x.shape[1] != k:
+        _same("x", x.shape, (n, k))
+    dev = _device(x, xq, out, ws)
+    sizes, total = _slice_array(tuple(slice_sizes))
+    if len(sizes) != L or total != N:
         raise ValueError("slice sizes do not match the pools")
     xqp, ldxq, xsp, wsp, w_type = None, 0, None, None, torch.bfloat16
     if xq is not None:
@@ -155,24 +194,25 @@ def lora_linear(x: torch.Tensor, w: torch.Tensor, a_pool: torch.Tensor, b_pool: 
             raise ValueError("xq needs x_scale and w_scale")
         xqp, ldxq = _rows(xq, "xq", torch.float8_e4m3fn)
         _same("xq", xq.shape, (n, k))
-        _same("x_scale", x_scale.shape, (n,))
-        _same("w_scale", w_scale.shape, (N,))
-        xsp, wsp = _dev(x_scale, "x_scale", torch.float32), _dev(w_scale, "w_scale", torch.float32)
+        xsp = _arg(x_scale, "x_scale", torch.float32, (n,), dev)
+        wsp = _arg(w_scale, "w_scale", torch.float32, (N,), dev)
         w_type = torch.float8_e4m3fn
     elif x_scale is not None or w_scale is not None:
         raise ValueError("x_scale and w_scale belong to the 8-bit form, which needs xq")
     if out is None:
-        out = torch.empty((n, N), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((n, N))
+        yp, ldy = out.data_ptr(), N
     else:
         _same("out", out.shape, (n, N))
-    yp, ldy = _rows(out, "out", torch.bfloat16)
+        yp, ldy = _rows(out, "out", torch.bfloat16)
     if ws is None:
         ws = linear_workspace(n, k, N, L, R, x.device)
-    st = lib().step_lora_linear(xp, ldx, n, k, xqp, ldxq, xsp, _dev(w, "w", w_type), wsp,
-                                _dev(a_pool, "a_pool", torch.bfloat16), _dev(b_pool, "b_pool", torch.bfloat16),
-                                _dev(scale, "scale", torch.float32), S, L, (_c_i32 * L)(*slice_sizes), R,
-                                _dev(slot, "slot", torch.int32), yp, ldy, _dev(ws, "ws", torch.uint8), ws.numel(),
-                                _stream(stream))
+    st = lib().step_lora_linear(xp, ldx, n, k, xqp, ldxq, xsp, _arg(w, "w", w_type, (N, k), dev), wsp,
+                                _arg(a_pool, "a_pool", torch.bfloat16, (S, L, R, k), dev),
+                                _arg(b_pool, "b_pool", torch.bfloat16, (S, N, R), dev),
+                                _arg(scale, "scale", torch.float32, (S,), dev), S, L, sizes, R,
+                                _arg(slot, "slot", torch.int32, (n,), dev), yp, ldy, _dev(ws, "ws", torch.uint8),
+                                ws.numel(), _raw_stream(dev))
     if st:
         _check("step_lora_linear", st)
     return out
@@ -197,24 +237,23 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, *, 
     """Per row of logits ([n, v], bf16 or float32): the log probability and the
     rank of tokens[i] (int32; negative: none asked for), the entropy, and the
     `top` most likely tokens with their log probabilities."""
+    if stream is not None:
+        return _on(stream, token_logprobs, (logits, tokens, top), dict(ws=ws))
     lp, ld = _rows(logits, "logits", torch.bfloat16, torch.float32)
     n, v = logits.shape
-    _same("tokens", tokens.shape, (n,))
-    dev = logits.device
-    # one block for the five outputs: fewer allocations in a decode step
-    flat = torch.empty((n * (3 + 2 * top),), dtype=torch.float32, device=dev)
-    logprob, rank, entropy = flat[:n], flat[n:2 * n].view(torch.int32), flat[2 * n:3 * n]
-    ids = best = None
+    dev = _device(logits, ws)
+    tp = _arg(tokens, "tokens", torch.int32, (n,), dev)
+    logprob, rank = tokens.new_empty(n, dtype=torch.float32), tokens.new_empty(n)
+    entropy = tokens.new_empty(n, dtype=torch.float32)
+    ids = best = ip = bp = None
     if top > 0:
-        ids = flat[3 * n:(3 + top) * n].view(torch.int32).view(n, top)
-        best = flat[(3 + top) * n:].view(n, top)
+        ids, best = tokens.new_empty((n, top)), tokens.new_empty((n, top), dtype=torch.float32)
+        ip, bp = ids.data_ptr(), best.data_ptr()
     if ws is None:
-        ws = logprobs_workspace(n, v, top, dev)
-    base = flat.data_ptr()
-    st = lib().step_token_logprobs(lp, ld, 1 if logits.dtype == torch.float32 else 0, n, v,
-                                   _dev(tokens, "tokens", torch.int32), top, base, base + 4 * n, base + 8 * n,
-                                   base + 12 * n if top > 0 else None, base + (12 + 4 * top) * n if top > 0 else None,
-                                   _dev(ws, "ws", torch.uint8), ws.numel(), _stream(stream))
+        ws = logprobs_workspace(n, v, top, logits.device)
+    st = lib().step_token_logprobs(lp, ld, 1 if logits.dtype == torch.float32 else 0, n, v, tp, top,
+                                   logprob.data_ptr(), rank.data_ptr(), entropy.data_ptr(), ip, bp,
+                                   _dev(ws, "ws", torch.uint8), ws.numel(), _raw_stream(dev))
     if st:
         _check("step_token_logprobs", st)
     return LogprobResult(logprob, rank, entropy, ids, best)
