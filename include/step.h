@@ -85,6 +85,9 @@ size_t step_lora_linear_workspace_bytes(int32_t n, int32_t k, int32_t out, int32
  * the adapters still read x.  Without it xq, x_scale and w_scale are null.
  * slice_sizes is a [host] array of num_slices widths.  The products with
  * b_pool take the fp32 inner sums as two bf16 terms (16 bits of mantissa).
+ * An infinity or NaN in an adapter or a row of x reaches no row but its own:
+ * in b_pool[s][c] it makes y[i][c] NaN or infinite for the rows of slot s, in
+ * x[i] or an inner sum it may do so for any column of that row.
  * Limits: k a multiple of 16 in [16, 1 << 18]; every slice width a multiple
  * of 8; 1 <= num_slices <= 8; out <= 1 << 24; max_rank a multiple of 8 in
  * [8, 128]; 1 <= num_slots <= 8192; n <= 1 << 18; ldx and ldy multiples of 8

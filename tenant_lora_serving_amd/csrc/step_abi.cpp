@@ -102,8 +102,7 @@ int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const
     a.slot = slot;
     a.y = y;
     a.ldy = ldy;
-    return launched((plan.tiled ? st::launch_lora_linear_tiled : st::launch_lora_linear)(
-        a, plan, ws, static_cast<hipStream_t>(stream)));
+    return launched(st::launch_lora_linear(a, plan, ws, static_cast<hipStream_t>(stream)));
 }
 
 size_t step_token_logprobs_workspace_bytes(int32_t n, int32_t v, int32_t top) {

@@ -58,7 +58,7 @@ struct ScoreArgs {
 };
 hipError_t launch_token_logprobs(const ScoreArgs &a, const ScorePlan &plan, void *ws, hipStream_t st);
 
-// Longest k at which 8-bit rows are multiplied as bf16 (step_linear.h); never tiled.
+// Longest k at which 8-bit rows are multiplied as bf16 (step_linear.h); never in large tiles.
 constexpr int kExactK = 256;
 
 struct LinearArgs {
@@ -79,15 +79,28 @@ struct LinearArgs {
     uint16_t *y;
     int64_t ldy;
 };
-// How a projection runs and what its workspace holds.  tiled: the rows' order
-// by slot and their slots in it (row_words words each), then the inner sums
-// of the rows in that order; otherwise the inner sums alone.
+// How a projection runs: in small tiles of the rows as they come (at most
+// kUnsortedRows of them) or of the rows sorted by slot, or in large tiles of
+// the sorted rows.  The workspace holds the sorted rows' numbers and their
+// slots (row_words words each), then the inner sums.
+enum LinearPath { kRowsPath, kSortedRowsPath, kTiledPath };
+constexpr int kUnsortedRows = 256;
 struct LinearPlan {
-    bool tiled;
+    LinearPath path;
     size_t row_words, total_bytes;
 };
 LinearPlan linear_plan(int n, int k, int out, int num_slices, int R);
+struct LinearSpace {
+    int32_t *perm, *key_of;
+    uint16_t *xab;
+};
+inline LinearSpace linear_space(const LinearPlan &plan, void *ws) {
+    int32_t *perm = static_cast<int32_t *>(ws), *key_of = perm + plan.row_words;
+    return {perm, key_of, reinterpret_cast<uint16_t *>(key_of + plan.row_words)};
+}
 hipError_t launch_lora_linear(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st);
-hipError_t launch_lora_linear_tiled(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st);
+void launch_sort_rows(const LinearArgs &a, const LinearSpace &s, hipStream_t st);
+void launch_sorted_inner(const LinearArgs &a, const LinearSpace &s, hipStream_t st);
+void launch_lora_linear_tiled(const LinearArgs &a, const LinearSpace &s, hipStream_t st);
 
 }  // namespace st

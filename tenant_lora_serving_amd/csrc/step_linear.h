@@ -205,14 +205,61 @@ __device__ __forceinline__ u32x4_t pack8(const float *v) {
 
 // The inner sums scale[s] x A_s^T travel as two bf16 terms a value (16 bits of
 // mantissa; one term alone would add an error of the size of the result's own
-// rounding): [row][slice][R rounded values, then R rests].
+// rounding): [row][slice][R rounded values, then R rests].  An infinity or NaN
+// has rest 0; a finite value that would round to infinity is cut instead.
 __device__ __forceinline__ void put_inner8(uint16_t *xab, int64_t row, int c, int num_slices, int R, const float *v) {
-    float rest[8];
+    float main[8], rest[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) rest[e] = v[e] - tl::bf16_round(v[e]);
+    for (int e = 0; e < 8; ++e) {
+        const bool finite = fabsf(v[e]) < INFINITY;
+        main[e] = tl::bf16_round(v[e]);
+        if (finite && !(fabsf(main[e]) < INFINITY)) main[e] = tl::bf_hi(__float_as_uint(v[e]));
+        rest[e] = finite ? v[e] - main[e] : 0.0f;
+    }
     uint16_t *to = xab + ((row * num_slices + c / R) * 2) * R + c % R;
-    tl::st16(to, pack8(v));
+    tl::st16(to, pack8(main));
     tl::st16(to + R, pack8(rest));
+}
+
+// ---------------------------------------------------------------- adapters in shared tiles
+// A product with one slot's B multiplies the rows of other slots by zero.
+// That is nothing unless the B holds an infinity or NaN, which must not reach
+// them: fragments are looked through for one (exponent bits all set), ...
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2_t larger_magnitude(u16x2_t m, uint32_t w) {
+    return __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w & 0x7fff7fffu));
+}
+__device__ __forceinline__ u16x2_t larger_magnitude(u16x2_t m, const u32x4_t v) {
+    return larger_magnitude(larger_magnitude(larger_magnitude(larger_magnitude(m, v.x), v.y), v.z), v.w);
+}
+__device__ __forceinline__ bool not_finite(u16x2_t m) { return m.x >= 0x7f80 || m.y >= 0x7f80; }
+// ... what is found is taken as zero, ...
+__device__ __forceinline__ void drop_not_finite(u32x4_t &v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t w = v[e];
+        if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+        if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+        v[e] = w;
+    }
+}
+// ... and the results that it belongs to become NaN after the tile is stored.
+// By every thread of the workgroup; slots: of the tile's rows m0 .. m0 + rows.
+template <int THREADS>
+__device__ __forceinline__ void mark_broken(const LinearArgs &a, int out, int m0, int rows, int c0, int cols,
+                                            const int32_t *perm, const int32_t *slots) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the results themselves are stored
+    __syncthreads();
+#pragma unroll 1
+    for (int t = threadIdx.x; t < rows * cols; t += THREADS) {
+        const int m = m0 + t / cols, c = c0 + t % cols, slot = slots[m];
+        if (slot < 0 || slot >= a.num_slots) continue;
+        const uint16_t *B = a.b_pool + ((int64_t)slot * out + c) * a.R;
+        u16x2_t big = {};
+#pragma unroll 1
+        for (int r = 0; r < a.R; r += 8) big = larger_magnitude(big, tl::ld16(B + r));
+        if (not_finite(big)) a.y[(int64_t)(perm ? perm[m] : m) * a.ldy + c] = 0x7fc0;
+    }
 }
 
 }  // namespace st

@@ -1,17 +1,23 @@
 // step_linear.hip -- step_lora_linear: the shared projection with every row's
 // adapter added,
 //
-//     y[i] = x[i] W^T + scale[s] (x[i] A_s^T) B_s^T,   s = slot[i].
+//     y[i] = x[i] W^T + scale[s] (x[i] A_s^T) B_s^T,   s = slot[i],
 //
-// Two launches.  The first computes the inner sums xa[i] = scale[s] x[i] A_s^T
+// in small tiles, for few rows or a small product.
+//
+// Two launches (and, past kUnsortedRows rows, the sort of the rows by slot
+// before them).  The first computes the inner sums xa[i] = scale[s] x[i] A_s^T
 // of each slot's rows.  The second computes tiles of x W^T and, before it
 // rounds, adds xa B_s^T for each slot that a tile's rows name, as matrix
-// products in which only that slot's rows are not zero.
+// products in which only that slot's rows are not zero.  (As one launch, with
+// a counter between the two, q, k and v of one row took 14.9 instead of 17.9
+// us, but those of 256 rows 55 instead of 45: the waiting workgroups' reads of
+// the counter come one after another.)
 //
-// With up to some hundred rows the product is bound by reading: W from memory,
-// x from L2 by every workgroup.  The waves of a workgroup share one tile and
-// take every kWaves-th line of k through rings of their own, so nothing that a
-// wave loads is another's too and there is no barrier in the loop.  The waves'
+// The product is bound by reading: W from memory, x from L2 by every
+// workgroup.  The waves of a workgroup share one tile and take every
+// kWaves-th line of k through rings of their own, so nothing that a wave
+// loads is another's too and there is no barrier in the loop.  The waves'
 // sums meet in shared memory once, at the end.
 #include "step_linear.h"
 
@@ -20,41 +26,74 @@ namespace st {
 namespace {
 
 // ---------------------------------------------------------------- inner sums
-// 16 rows of slot blockIdx.x (the blockIdx.y-th 16 of them) times 64 of the
-// num_slices * R rows of A_s, 16 of these a workgroup: one CU alone draws no
-// more than some 30 GB/s from memory, so A_s is spread over many.  Eight waves
-// split k, so that each has only a few lines to wait for.
-constexpr int kInWaves = 8, kInThreads = kInWaves * kWave, kInNT = 1, kInSlots = 4;
-__global__ __launch_bounds__(kInThreads) void inner_kernel(LinearArgs a, uint16_t *xab) {
-    using Part = Partials<kInNT, 1>;
-    __shared__ int rows[16];
-    __shared__ int before[kInWaves + 1];
-    using Ring = LineRing<kInNT, 1, kInSlots>;
-    __shared__ __align__(16) char rings[kInWaves * Ring::kBytes];
-    __shared__ float red[kInWaves * Part::kFloats];
-    const int slot = blockIdx.x, r_first = blockIdx.y * 16, c0 = blockIdx.z * Part::kCols;
-    const int lane = tl::lane_id(), tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
-    const int LR = a.num_slices * a.R, kbytes = a.k * 2, lines = (kbytes + kLine - 1) / kLine;
+constexpr int kInWaves = 8, kInThreads = kInWaves * kWave;
 
-    // the slot's rows r_first .. r_first + 16, in order
-    int found = 0;
-    for (int r0 = 0; r0 < a.n && found < r_first + 16; r0 += kInThreads) {
-        const bool hit = r0 + tid < a.n && a.slot[r0 + tid] == slot;
-        const uint64_t mask = __ballot(hit);
-        if (lane == 0) before[wave] = __popcll(mask);
-        __syncthreads();
-        int at = found + __popcll(mask & tl::lanemask_lt()), all = 0;
+// The t-th group of up to 16 rows of one slot, numbered slot by slot; count 0
+// past the last group.  Lane m < count holds row m's number.  Every wave finds
+// it by itself, from ballots: ranks through LDS, with their barriers, took
+// 4 us more for some hundred rows.
+struct Group {
+    int slot, count, row;
+};
+__device__ __forceinline__ Group find_group(const LinearArgs &a, int t) {
+    constexpr int kChunks = kUnsortedRows / kWave;
+    const int lane = tl::lane_id();
+    int s[kChunks], before = 0;
+    uint64_t todo[kChunks], same[kChunks];
 #pragma unroll
-        for (int w = 0; w < kInWaves; ++w) {
-            at += w < wave ? before[w] : 0;
-            all += before[w];
-        }
-        if (hit && at >= r_first && at < r_first + 16) rows[at - r_first] = r0 + tid;
-        found += all;
-        __syncthreads();
+    for (int c = 0; c < kChunks; ++c) {
+        s[c] = c * kWave + lane < a.n ? a.slot[c * kWave + lane] : -1;
+        todo[c] = __ballot(s[c] >= 0 && s[c] < a.num_slots);
     }
-    const int count = min(found - r_first, 16);
-    if (count <= 0) return;
+    for (;;) {
+        int slot = -1;
+#pragma unroll
+        for (int c = kChunks - 1; c >= 0; --c)
+            if (todo[c]) slot = __builtin_amdgcn_readlane(s[c], __builtin_ctzll(todo[c]));
+        if (slot < 0) return {-1, 0, 0};
+        int rows = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            same[c] = __ballot(s[c] == slot);
+            todo[c] &= ~same[c];
+            rows += __popcll(same[c]);
+        }
+        const int groups = (rows + 15) / 16;
+        if (t >= before + groups) {
+            before += groups;
+            continue;
+        }
+        // each of the group's lanes hands its row's number + 1 to the lane of
+        // its place in the group, the others a 0 to the last lane
+        const int first = (t - before) * 16;
+        int at = -first, row = 0;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int i = at + __popcll(same[c] & tl::lanemask_lt());
+            const bool mine = (same[c] >> lane & 1) && i >= 0 && i < 16;
+            row = max(row, __builtin_amdgcn_ds_permute((mine ? i : kWave - 1) * 4, mine ? c * kWave + lane + 1 : 0));
+            at += __popcll(same[c]);
+        }
+        return {slot, min(rows - first, 16), row - 1};
+    }
+}
+
+// A group of rows by 16 NT of the num_slices * R rows of A_s.  Eight waves
+// split k, so that each has only a few lines to wait for.
+template <int NT, int SLOTS>
+__global__ __launch_bounds__(kInThreads) void inner_kernel(LinearArgs a, uint16_t *xab) {
+    using Part = Partials<NT, 1>;
+    using Ring = LineRing<NT, 1, SLOTS>;
+    constexpr int kShared = Ring::kBytes > Part::kFloats * 4 ? Ring::kBytes : Part::kFloats * 4;
+    __shared__ __align__(16) char shared[kInWaves * kShared];
+    float *red = reinterpret_cast<float *>(shared);
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
+    const int LR = a.num_slices * a.R, kbytes = a.k * 2, lines = (kbytes + kLine - 1) / kLine;
+    const int c0 = blockIdx.y * Part::kCols;
+    const Group group = find_group(a, blockIdx.x);
+    const int slot = __builtin_amdgcn_readfirstlane(group.slot), count = __builtin_amdgcn_readfirstlane(group.count);
+    const int row = group.row;
+    if (count == 0) return;
 
     const uint16_t *A = a.a_pool + ((int64_t)slot * LR + c0) * a.k;
     const i32x4_t wr = words_rsrc(A, (uint32_t)(min(LR - c0, Part::kCols) * kbytes));
@@ -64,32 +103,38 @@ __global__ __launch_bounds__(kInThreads) void inner_kernel(LinearArgs a, uint16_
 #pragma unroll
     for (int u = 0; u < Ring::kW; ++u) wo[u] = c0 + Ring::row(u) < LR ? (uint32_t)(Ring::row(u) * kbytes) : kOob;
 #pragma unroll
-    for (int u = 0; u < Ring::kX; ++u)
-        xo[u] = Ring::row(u) < count ? (uint32_t)((int64_t)rows[Ring::row(u)] * a.ldx * 2) : kOob;
-    f32x4_t acc[kInNT][1] = {};
-    ring_product<kBf16, kInNT, 1, kInSlots>(wr, wo, xr, xo, rings + wave * Ring::kBytes, wave, kInWaves, lines, kbytes,
-                                            acc);
+    for (int u = 0; u < Ring::kX; ++u) {
+        const int m = Ring::row(u), r = __shfl(row, m);
+        xo[u] = m < count ? (uint32_t)((int64_t)r * a.ldx * 2) : kOob;
+    }
+    f32x4_t acc[NT][1] = {};
+    ring_product<kBf16, NT, 1, SLOTS>(wr, wo, xr, xo, shared + wave * Ring::kBytes, wave, kInWaves, lines, kbytes, acc);
+    __syncthreads();  // (the partial sums lie over the rings)
     Part::put(red, wave, acc);
     __syncthreads();
-    for (int t = tid; t < 16 * Part::kCols / 8; t += kInThreads) {
-        const int m = t / (Part::kCols / 8), c = t % (Part::kCols / 8) * 8;
-        if (m >= count || c0 + c >= LR) continue;
+    constexpr int kVecs = Part::kCols / 8;
+    const int m = tid / kVecs % 16, c = tid % kVecs * 8, r = __shfl(row, m);
+    if (tid < 16 * kVecs && m < count && c0 + c < LR) {
         float v[8];
-        Part::sum8<kInWaves>(red, m, c, v);
+        Part::template sum8<kInWaves>(red, m, c, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= scale;
-        put_inner8(xab, rows[m], c0 + c, a.num_slices, a.R, v);
+        put_inner8(xab, r, c0 + c, a.num_slices, a.R, v);
     }
 }
 
 // ---------------------------------------------------------------- the product
+// SLOTS lines in a wave's ring.
 constexpr int kWaves = 4, kThreads = kWaves * kWave;
-
-// SLOTS lines in a wave's ring; IT adapter steps in flight.
-template <Form F, int MT, int NT, int SLOTS, int IT>
-__global__ __launch_bounds__(kThreads) void linear_kernel(LinearArgs a, const uint16_t *xab, int out) {
+struct Inner {
+    const int32_t *perm, *key_of;  // sorted rows: their row numbers and slots
+    const uint16_t *xab;
+};
+template <Form F, int MT, int NT, int SLOTS, bool SORTED>
+__global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, int out) {
     using Part = Partials<NT, MT>;
     using Ring = LineRing<NT, MT, SLOTS>;
+    constexpr int IT = 2;  // adapter steps on the way
     constexpr int kShared = Ring::kBytes > Part::kFloats * 4 ? Ring::kBytes : Part::kFloats * 4;
     __shared__ __align__(16) char shared[kWaves * kShared];
     float *red = reinterpret_cast<float *>(shared);  // over the rings, when they are done with
@@ -101,25 +146,30 @@ __global__ __launch_bounds__(kThreads) void linear_kernel(LinearArgs a, const ui
     const int c0 = (on_xcd / m_tiles * 8 + blockIdx.x % 8) * Part::kCols, m0 = on_xcd % m_tiles * Part::kRows;
     if (c0 >= out) return;
     const int rows = min(a.n - m0, Part::kRows), cols = min(out - c0, Part::kCols);
+    const int my_row = lane < rows ? (SORTED ? h.perm[m0 + lane] : m0 + lane) : 0;
+    int my_slot = lane < rows ? (SORTED ? h.key_of[m0 + lane] : a.slot[m0 + lane]) : -1;
+    if (my_slot >= a.num_slots) my_slot = -1;
 
     constexpr bool FP8 = F != kBf16;
     constexpr int esz = FP8 ? 1 : 2;
     const int kbytes = a.k * esz, lines = (kbytes + kLine - 1) / kLine;
     const int64_t ldx = FP8 ? a.ldxq : a.ldx * 2;
-    const char *x = (FP8 ? (const char *)a.xq : (const char *)a.x) + m0 * ldx;
-    const i32x4_t xr = words_rsrc(x, (uint32_t)((rows - 1) * ldx + kbytes));
+    const i32x4_t xr = words_rsrc(FP8 ? (const void *)a.xq : (const void *)a.x,
+                                  (uint32_t)((int64_t)(a.n - 1) * ldx + kbytes));
     const i32x4_t wr = words_rsrc((const char *)a.w + (int64_t)c0 * kbytes, (uint32_t)(cols * kbytes));
     uint32_t wo[Ring::kW], xo[Ring::kX];
 #pragma unroll
     for (int u = 0; u < Ring::kW; ++u) wo[u] = Ring::row(u) < cols ? (uint32_t)(Ring::row(u) * kbytes) : kOob;
 #pragma unroll
-    for (int u = 0; u < Ring::kX; ++u) xo[u] = Ring::row(u) < rows ? (uint32_t)(Ring::row(u) * ldx) : kOob;
-    int my_slot = lane < rows ? a.slot[m0 + lane] : -1;
-    if (my_slot >= a.num_slots) my_slot = -1;
+    for (int u = 0; u < Ring::kX; ++u) {
+        const int m = Ring::row(u), r = SORTED ? __shfl(my_row, m) : m0 + m;
+        xo[u] = m < rows ? (uint32_t)((int64_t)r * ldx) : kOob;
+    }
     f32x4_t acc[NT][MT] = {};
     ring_product<F, NT, MT, SLOTS>(wr, wo, xr, xo, shared + wave * Ring::kBytes, wave, kWaves, lines, kbytes, acc);
 
     if constexpr (FP8) {
+        const float my_scale = lane < rows ? a.x_scale[my_row] : 0.0f;
         float ws[NT][4];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -130,8 +180,7 @@ __global__ __launch_bounds__(kThreads) void linear_kernel(LinearArgs a, const ui
             }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const int m = 16 * i + lane % 16;
-            const float xs = m < rows ? a.x_scale[m0 + m] : 0.0f;
+            const float xs = __shfl(my_scale, 16 * i + lane % 16);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -139,63 +188,78 @@ __global__ __launch_bounds__(kThreads) void linear_kernel(LinearArgs a, const ui
         }
     }
 
-    // ---- the adapters, in steps of 32 of the 2 R terms of one slice of one
-    // slot (R rounded inner sums and R rests, against the same B twice); the
-    // waves take every kWaves-th slot, IT steps at a time.
+    // ---- the adapters, slice by slice, in steps of 32 of the 2 R terms of one
+    // slot (R rounded inner sums and R rests, against the same B twice), IT
+    // steps on the way.  A wave takes the slots that are its number modulo
+    // kWaves: so a row's sums meet in the same order whatever other rows share
+    // its tile, and the order of the sorted rows changes no result.
     const int chunks = a.R / 8;
     int first_slice = 0, end_slice = a.num_slices;
     while (a.slice_off[first_slice + 1] <= c0) ++first_slice;
     while (end_slice > first_slice + 1 && a.slice_off[end_slice - 1] >= c0 + cols) --end_slice;
-    uint64_t left = __ballot(my_slot >= 0), same = 0;
-    int slot = -1, slice = 0, q0 = 0;
-    auto next_slot = [&](int skip) {  // skips `skip` slots, then takes one
-        slice = first_slice;
-        q0 = 0;
-        do {
-            if (!left) {
-                slot = -1;
-                same = 0;
-                return;
-            }
-            slot = __builtin_amdgcn_readlane(my_slot, __builtin_ctzll(left));
-            same = __ballot(my_slot == slot);
-            left &= ~same;
-        } while (skip--);
-    };
-    next_slot(wave);
-    while (slot >= 0) {
+    const uint64_t with_slot = __ballot(my_slot >= 0), mine = __ballot(my_slot >= 0 && my_slot % kWaves == wave);
+    int *any_broken = reinterpret_cast<int *>(shared + kWaves * kShared) - 1;  // past what is written below
+    static_assert(kWaves * Part::kFloats * 4 <= kWaves * kShared - 4, "past the partial sums");
+    __syncthreads();
+    if (tid == 0) *any_broken = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int slice = with_slot ? first_slice : end_slice; slice < end_slice; ++slice) {
+        const int lo = a.slice_off[slice] - c0, hi = min(a.slice_off[slice + 1] - c0, cols);
+        uint64_t todo = mine, same = 0;
+        int slot = -1, q0 = 0;
+        auto next_slot = [&]() {
+            q0 = 0;
+            slot = todo ? __builtin_amdgcn_readlane(my_slot, __builtin_ctzll(todo)) : -1;
+            same = slot >= 0 ? __ballot(my_slot == slot) : 0;
+            todo &= ~same;
+        };
         u32x4_t bf[IT][NT], xf[IT][MT];
         uint64_t who[IT];
+        auto load_steps = [&]() {
 #pragma unroll
-        for (int s = 0; s < IT; ++s) {
-            who[s] = same;
-            const int q = q0 + lane / 16, r = (q >= chunks ? q - chunks : q) * 8;
-            const bool in = q < 2 * chunks && slot >= 0;
-            const uint16_t *B = a.b_pool + ((int64_t)slot * out + c0) * a.R + r;
-            const uint16_t *X = xab + ((int64_t)m0 * a.num_slices + slice) * 2 * a.R + q * 8;
-            const int lo = a.slice_off[slice] - c0, hi = min(a.slice_off[slice + 1] - c0, cols);
+            for (int s = 0; s < IT; ++s) {
+                who[s] = same;
+                const int q = q0 + lane / 16, r = (q >= chunks ? q - chunks : q) * 8;
+                const bool in = q < 2 * chunks && slot >= 0;
+                const uint16_t *B = a.b_pool + ((int64_t)slot * out + c0) * a.R + r;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int c = 16 * j + lane % 16;
-                bf[s][j] = in && c >= lo && c < hi ? tl::ld16(B + (int64_t)c * a.R) : tl::zero4();
+                for (int j = 0; j < NT; ++j) {
+                    const int c = 16 * j + lane % 16;
+                    bf[s][j] = in && c >= lo && c < hi ? tl::ld16(B + (int64_t)c * a.R) : tl::zero4();
+                }
+                const uint16_t *X = h.xab + ((int64_t)m0 * a.num_slices + slice) * 2 * a.R + 8 * q;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int m = 16 * i + lane % 16;
+                    xf[s][i] = in && (same >> m & 1) ? tl::ld16(X + (int64_t)m * a.num_slices * 2 * a.R) : tl::zero4();
+                }
+                if (slot >= 0 && (q0 += 4) >= 2 * chunks) next_slot();
             }
+        };
+        next_slot();
+        load_steps();
+#pragma unroll 1
+        while (who[0]) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int m = 16 * i + lane % 16;
-                xf[s][i] = in && (same >> m & 1) ? tl::ld16(X + (int64_t)m * a.num_slices * 2 * a.R) : tl::zero4();
-            }
-            if (slot >= 0 && (q0 += 4) >= 2 * chunks) {
-                q0 = 0;
-                if (++slice == end_slice) next_slot(kWaves - 1);
-            }
-        }
+            for (int s = 0; s < IT; ++s) {
+                u16x2_t big = {};
 #pragma unroll
-        for (int s = 0; s < IT; ++s)
+                for (int j = 0; j < NT; ++j) big = larger_magnitude(big, bf[s][j]);
+                if (__ballot(not_finite(big))) {
+                    *any_broken = 1;
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-                if (who[s] >> (16 * i) & 0xffff)
+                    for (int j = 0; j < NT; ++j) drop_not_finite(bf[s][j]);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    if (!(who[s] >> (16 * i) & 0xffff)) continue;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) acc[j][i] = tl::mfma_16x16x32(bf[s][j], xf[s][i], acc[j][i]);
+                }
+            }
+            load_steps();
+        }
     }
 
     __syncthreads();
@@ -206,41 +270,61 @@ __global__ __launch_bounds__(kThreads) void linear_kernel(LinearArgs a, const ui
         if (m >= rows || c >= cols) continue;
         float v[8];
         Part::template sum8<kWaves>(red, m, c, v);
-        tl::st16(a.y + (int64_t)(m0 + m) * a.ldy + c0 + c, pack8(v));
+        const int64_t r = SORTED ? h.perm[m0 + m] : m0 + m;
+        tl::st16(a.y + r * a.ldy + c0 + c, pack8(v));
     }
+    if (*any_broken)
+        mark_broken<kThreads>(a, out, m0, rows, c0, cols, SORTED ? h.perm : nullptr, SORTED ? h.key_of : a.slot);
 }
 
 template <Form F, int MT, int NT, int SLOTS>
-hipError_t go(const LinearArgs &a, const uint16_t *xab, int out, hipStream_t st) {
+void go(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
     const int m_tiles = (a.n + 16 * MT - 1) / (16 * MT), c_tiles = (out + 16 * NT - 1) / (16 * NT);
-    linear_kernel<F, MT, NT, SLOTS, 2>
-        <<<dim3((unsigned)((c_tiles + 7) / 8 * 8) * m_tiles), kThreads, 0, st>>>(a, xab, out);
-    return hipGetLastError();
+    const dim3 grid((unsigned)((c_tiles + 7) / 8 * 8) * m_tiles);
+    if constexpr (MT == 4) {
+        if (h.perm) {
+            rows_kernel<F, MT, NT, SLOTS, true><<<grid, kThreads, 0, st>>>(a, h, out);
+            return;
+        }
+    }
+    rows_kernel<F, MT, NT, SLOTS, false><<<grid, kThreads, 0, st>>>(a, h, out);
 }
 
 template <Form F>
-hipError_t pick(const LinearArgs &a, const uint16_t *xab, int out, hipStream_t st) {
+void pick(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
     const int tiles = (out + 15) / 16;
-    if (a.n <= 16) return tiles > 768 ? go<F, 1, 2, 3>(a, xab, out, st) : go<F, 1, 1, 4>(a, xab, out, st);
-    if (a.n <= 32) return tiles > 768 ? go<F, 2, 4, 2>(a, xab, out, st) : go<F, 2, 1, 4>(a, xab, out, st);
+    if (a.n <= 16) return tiles > 768 ? go<F, 1, 2, 3>(a, h, out, st) : go<F, 1, 1, 4>(a, h, out, st);
+    if (a.n <= 32) return tiles > 768 ? go<F, 2, 4, 2>(a, h, out, st) : go<F, 2, 1, 4>(a, h, out, st);
     const int m_tiles = (a.n + 63) / 64;
     auto rounds = [&](int nt) { return ((tiles + nt - 1) / nt * m_tiles + 255) / 256 * (4 + nt + 3); };
-    if (rounds(6) <= rounds(4) && rounds(6) <= rounds(2)) return go<F, 4, 6, 2>(a, xab, out, st);
-    return rounds(4) <= rounds(2) ? go<F, 4, 4, 2>(a, xab, out, st) : go<F, 4, 2, 3>(a, xab, out, st);
+    if (rounds(6) <= rounds(4) && rounds(6) <= rounds(2)) return go<F, 4, 6, 2>(a, h, out, st);
+    return rounds(4) <= rounds(2) ? go<F, 4, 4, 2>(a, h, out, st) : go<F, 4, 2, 3>(a, h, out, st);
 }
 
 }  // namespace
 
 hipError_t launch_lora_linear(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st) {
-    (void)plan;
-    uint16_t *xab = static_cast<uint16_t *>(ws);
-    const int out = a.slice_off[a.num_slices], cols = 16 * kInNT;
-    inner_kernel<<<dim3(a.num_slots, (a.n + 15) / 16, (a.num_slices * a.R + cols - 1) / cols), kInThreads, 0, st>>>(
-        a, xab);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.xq && a.k <= kExactK) return go<kE4m3AsBf16, 4, 4, 2>(a, xab, out, st);
-    return a.xq ? pick<kE4m3>(a, xab, out, st) : pick<kBf16>(a, xab, out, st);
+    const int out = a.slice_off[a.num_slices];
+    const LinearSpace s = linear_space(plan, ws);
+    if (plan.path != kRowsPath) launch_sort_rows(a, s, st);
+    if (plan.path != kRowsPath) {
+        launch_sorted_inner(a, s, st);
+    } else {
+        // groups of up to 16 rows of one slot: every slot ends one that is not full
+        const int most = a.n / 16 + a.num_slots, groups = a.n < most ? a.n : most, LR = a.num_slices * a.R;
+        if (groups * ((LR + 15) / 16) <= 512) inner_kernel<1, 4><<<dim3(groups, (LR + 15) / 16), kInThreads, 0, st>>>(a, s.xab);
+        else inner_kernel<4, 2><<<dim3(groups, (LR + 63) / 64), kInThreads, 0, st>>>(a, s.xab);
+    }
+    if (plan.path == kTiledPath) {
+        launch_lora_linear_tiled(a, s, st);
+        return hipGetLastError();
+    }
+    const bool sorted = plan.path == kSortedRowsPath;
+    const Inner h{sorted ? s.perm : nullptr, s.key_of, s.xab};
+    if (a.xq && a.k <= kExactK) pick<kE4m3AsBf16>(a, h, out, st);
+    else if (a.xq) pick<kE4m3>(a, h, out, st);
+    else pick<kBf16>(a, h, out, st);
+    return hipGetLastError();
 }
 
 }  // namespace st

@@ -66,7 +66,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const int32_t *slot,
 
 // ---------------------------------------------------------------- inner sums
 // scale[s] x A_s^T for 32 sorted rows and 64 of the num_slices * R rows of
-// A_s, for each slot that the rows name; written as [row][slice][R rounded
+// A_s, for each gridDim.z-th slot that the rows name; written as [row][slice][R rounded
 // values, R rests] in bf16.  Four waves take every fourth line of k.
 constexpr int kInMT = 2, kInNT = 4, kInSlots = 2, kInRows = 16 * kInMT, kInCols = 16 * kInNT;
 __global__ __launch_bounds__(256) void sorted_inner_kernel(LinearArgs a, const int32_t *perm, const int32_t *key_of,
@@ -88,10 +88,11 @@ __global__ __launch_bounds__(256) void sorted_inner_kernel(LinearArgs a, const i
     for (int u = 0; u < Ring::kW; ++u)
         wo[u] = c0 + Ring::row(u) < LR ? (uint32_t)(Ring::row(u) * kbytes) : kOob;
     uint64_t left = __ballot(my_key < a.num_slots);
-    while (left) {
+    for (unsigned nth = 0; left; ++nth) {
         const int slot = __builtin_amdgcn_readlane(my_key, __builtin_ctzll(left));
         const uint64_t same = __ballot(my_key == slot);
         left &= ~same;
+        if (nth % gridDim.z != blockIdx.z) continue;
         const uint16_t *A = a.a_pool + ((int64_t)slot * LR + c0) * a.k;
         const i32x4_t wr = words_rsrc(A, (uint32_t)(min(LR - c0, kInCols) * kbytes));
 #pragma unroll
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int
     if (tid < BM) keys[tid] = tid < rows ? key_of[m0 + tid] : a.num_slots;
     __syncthreads();
 
-    static_assert(F != kE4m3AsBf16, "short k is not tiled");
+    static_assert(F != kE4m3AsBf16, "short k is not tiled: its widened fragments do not fit beside the sums");
     constexpr int esz = F == kBf16 ? 2 : 1;
     const int kbytes = a.k * esz, lines = (kbytes + kLine - 1) / kLine;
     const int64_t ldx = F == kBf16 ? a.ldx * 2 : a.ldxq;
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int
         }
     };
     const int live = rows - wm * 128;  // rows of this wave
-    auto multiply = [&](auto form, int ha, int hb) {
+    auto multiply = [&](auto form, int ha, int hb) __attribute__((always_inline)) {
         barrier();
         if (live > ha * 64) {
             __builtin_amdgcn_s_setprio(1);
@@ -334,13 +335,27 @@ __global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int
     barrier();
     barrier();
     // The line t in buffer b.  whole: lines t + 1 and t + 2 are whole lines of x and W.
-    auto line_step = [&](auto form, auto whole, int t, int b) {
+    bool broken = false;
+    auto look_through = [&](int h) __attribute__((always_inline)) {
+        u16x2_t big = {};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) big = larger_magnitude(larger_magnitude(big, fb[h][j].a), fb[h][j].b);
+        if (!__ballot(not_finite(big))) return;
+        broken = true;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            drop_not_finite(fb[h][j].a);
+            drop_not_finite(fb[h][j].b);
+        }
+    };
+    auto line_step = [&](auto form, auto adapter, auto whole, int t, int b) __attribute__((always_inline)) {
         constexpr bool W = decltype(whole)::value;
         // phase 1: B0; starts A1 of the next line
         read_b(b, 0);
         if constexpr (W) start_whole(b ^ 1, t + 1, P1{});
         else start_any(b ^ 1, P1{});
         wait_loads<10>();
+        if constexpr (decltype(adapter)::value) look_through(0);
         multiply(form, 0, 0);
         // phase 2: B1; starts A0 of the line after it
         if constexpr (!W) advance();
@@ -348,6 +363,7 @@ __global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int
         if constexpr (W) start_whole(b, t + 2, P0{});
         else start_any(b, P0{});
         wait_loads<10>();
+        if constexpr (decltype(adapter)::value) look_through(1);
         multiply(form, 0, 1);
         // phase 3: A1
         read_a(b, 1);
@@ -364,14 +380,16 @@ __global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int
     };
     using Main = std::integral_constant<Form, F>;
     using Extra = std::integral_constant<Form, kBf16>;
+    using Yes = std::true_type;
+    using No = std::false_type;
     int t = 0;
     for (; t + 3 < kbytes / kLine; t += 2) {
-        line_step(Main{}, std::true_type{}, t, 0);
-        line_step(Main{}, std::true_type{}, t + 1, 1);
+        line_step(Main{}, No{}, Yes{}, t, 0);
+        line_step(Main{}, No{}, Yes{}, t + 1, 1);
     }
     if (t > 0) cur.line = t + 1;  // (line t + 1 is started but for its A1)
 #pragma unroll 1
-    for (; t < lines; ++t) line_step(Main{}, std::false_type{}, t, t & 1);
+    for (; t < lines; ++t) line_step(Main{}, No{}, No{}, t, t & 1);
     if constexpr (F != kBf16) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -393,7 +411,7 @@ __global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int
             }
     }
 #pragma unroll 1
-    for (; t < total; ++t) line_step(Extra{}, std::false_type{}, t, t & 1);
+    for (; t < total; ++t) line_step(Extra{}, Yes{}, No{}, t, t & 1);
     if (wave < 4) barrier();
     wait_loads<0>();  // nothing may still write LDS when the workgroup ends
 
@@ -410,6 +428,8 @@ __global__ __launch_bounds__(kThreads) void tiled_kernel(LinearArgs a, const int
                                                                tl::pack_bf16x2(acc[j][i][2], acc[j][i][3]));
         }
     }
+
+    if (__syncthreads_or(broken)) mark_broken<kThreads>(a, out, m0, rows, c0, cols, perm, key_of);
 }
 
 template <Form F>
@@ -421,16 +441,23 @@ void go(const LinearArgs &a, const int32_t *perm, const int32_t *key_of, const u
 
 }  // namespace
 
-hipError_t launch_lora_linear_tiled(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st) {
-    int32_t *perm = static_cast<int32_t *>(ws), *key_of = perm + plan.row_words;
-    uint16_t *xab = reinterpret_cast<uint16_t *>(key_of + plan.row_words);
+void launch_sort_rows(const LinearArgs &a, const LinearSpace &s, hipStream_t st) {
+    sort_kernel<<<1, kSortThreads, 0, st>>>(a.slot, a.n, a.num_slots, s.perm, s.key_of);
+}
+
+void launch_sorted_inner(const LinearArgs &a, const LinearSpace &s, hipStream_t st) {
+    const int tiles = (a.n + kInRows - 1) / kInRows, cols = (a.num_slices * a.R + kInCols - 1) / kInCols;
+    // 32 rows name 1 + S / tiles slots on average where all S are named alike;
+    // one workgroup for all of them took 95 us for 300 rows of 300 slots
+    const int split = 1 + a.num_slots / tiles;
+    sorted_inner_kernel<<<dim3(tiles, cols, split < kInRows ? split : kInRows), 256, 0, st>>>(a, s.perm, s.key_of,
+                                                                                              s.xab);
+}
+
+void launch_lora_linear_tiled(const LinearArgs &a, const LinearSpace &s, hipStream_t st) {
     const int out = a.slice_off[a.num_slices];
-    sort_kernel<<<1, kSortThreads, 0, st>>>(a.slot, a.n, a.num_slots, perm, key_of);
-    sorted_inner_kernel<<<dim3((a.n + kInRows - 1) / kInRows, (a.num_slices * a.R + kInCols - 1) / kInCols), 256, 0,
-                          st>>>(a, perm, key_of, xab);
-    if (a.xq) go<kE4m3>(a, perm, key_of, xab, out, st);
-    else go<kBf16>(a, perm, key_of, xab, out, st);
-    return hipGetLastError();
+    if (a.xq) go<kE4m3>(a, s.perm, s.key_of, s.xab, out, st);
+    else go<kBf16>(a, s.perm, s.key_of, s.xab, out, st);
 }
 
 }  // namespace st

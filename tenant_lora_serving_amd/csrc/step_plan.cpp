@@ -34,10 +34,10 @@ ScorePlan score_plan(int n, int v, int top, int fp32) {
 
 LinearPlan linear_plan(int n, int k, int out, int num_slices, int R) {
     LinearPlan p{};
-    p.tiled = n > 1024 && k > kExactK;
     (void)out;
+    p.path = n > 1024 && k > kExactK ? kTiledPath : n > kUnsortedRows ? kSortedRowsPath : kRowsPath;
     const size_t inner = (size_t)n * num_slices * R * 2 * sizeof(uint16_t);
-    if (p.tiled) p.row_words = up256((size_t)n * sizeof(int32_t)) / sizeof(int32_t);
+    if (p.path != kRowsPath) p.row_words = up256((size_t)n * sizeof(int32_t)) / sizeof(int32_t);
     p.total_bytes = 2 * p.row_words * sizeof(int32_t) + up256(inner);
     return p;
 }

@@ -406,3 +406,97 @@ def test_refusals():
         step.token_logprobs(z, t.long())
     with pytest.raises(TypeError):
         step.token_logprobs(z.half(), t)
+
+
+# ---------------------------------------------------------------- projection: broken adapters, more paths
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [3, 30, 200, 700, 2100])
+def test_linear_broken_adapter_stays_with_its_rows(n, fp8):
+    """An infinity or NaN in one row, or in one tenant's adapter, shows in the
+    results that it belongs to and in no other row's (from an inner sum it may
+    reach the row's other columns, from B no other column)."""
+    print(f"linear broken n={n} fp8={fp8}", flush=True)
+    widths, k = (264, 120), 384
+    args, kw = linear_inputs(n, n, k, widths, 5, 16, fp8, slot=torch.arange(n, device="cuda") % 5)
+    x, w, a, b, scale, _, slot = args
+    clean = linear64(args, kw)
+    broken = torch.zeros(n, sum(widths), dtype=torch.bool, device="cuda")
+    x, a, b = x.clone(), a.clone(), b.clone()
+    x[1, 5] = math.inf                  # a row of slot 1
+    broken[1] = True
+    b[2, 7, 3], b[2, 300, 0] = math.nan, math.inf
+    broken[(slot == 2)[:, None] & (torch.arange(sum(widths), device="cuda") == 7)[None, :]] = True
+    broken[(slot == 2)[:, None] & (torch.arange(sum(widths), device="cuda") == 300)[None, :]] = True
+    a[3, 1, 2] = math.nan               # one of the second slice's inner sums
+    broken[(slot == 3)[:, None] & (torch.arange(sum(widths), device="cuda") >= 264)[None, :]] = True
+    got = step.lora_linear(x, w, a, b, scale, widths, slot, **kw)
+    assert not got[broken].isfinite().any()
+    y, tol = clean
+    rest = ~broken & (slot != 3)[:, None]
+    within(got[rest], y[rest], tol[rest], "the others")
+
+
+@pytest.mark.parametrize("n", [2, 100, 700, 1200])
+def test_linear_inner_sums_past_the_largest_bf16(n):
+    # 3.397e38 is finite in fp32 and rounds to infinity in bf16
+    k = 272
+    x = torch.zeros(n, k, device="cuda")
+    x[:, 0], x[:, 1] = 3.38953139e38, 7.5e35
+    a, b = torch.ones(1, 1, 8, k, device="cuda"), torch.full((1, 16, 8), 2.0 ** -100, device="cuda")
+    args = (x.bfloat16(), torch.zeros(16, k, device="cuda").bfloat16(), a.bfloat16(), b.bfloat16(),
+            torch.ones(1, device="cuda"), (16,), torch.zeros(n, dtype=torch.int32, device="cuda"))
+    check_linear(args, {}, step.lora_linear(*args), "large inner sums")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,k,widths,S,R", [
+    (33, 336, (16,), 40, 8), (511, 512, (136, 80), 512, 16), (512, 2064, (392,), 1, 24), (513, 64, (520, 8), 70, 128),
+    (640, 4096, (640, 128, 128), 32, 16), (900, 1536, (2056,), 6, 64), (1024, 272, (64, 64), 1024, 8),
+    (1100, 256, (512, 40), 9, 32), (1300, 16, (8,), 2, 8), (1800, 640, (72,), 16, 16), (5000, 96, (48,), 5000, 8),
+])
+def test_linear_more_shapes(n, k, widths, S, R, fp8):
+    print(f"linear n={n} k={k} widths={widths} S={S} R={R} fp8={fp8}", flush=True)
+    args, kw = linear_inputs(n + k, n, k, widths, S, R, fp8, pad=16 if n % 2 else 0)
+    check_linear(args, kw, step.lora_linear(*args, **kw), "linear")
+
+
+def test_one_workspace_through_every_path():
+    ws = step.linear_workspace(3000, 512, 512, 2, 64)
+    for n, k, widths, S, R in [(3000, 512, (264, 248), 9, 64), (4, 512, (64,), 3, 16), (700, 384, (72,), 30, 8),
+                               (4, 512, (64,), 3, 16), (300, 48, (16, 16), 7, 64), (3000, 512, (264, 248), 9, 64)]:
+        args, kw = linear_inputs(n, n, k, widths, S, R)
+        for _ in range(2):
+            check_linear(args, kw, step.lora_linear(*args, ws=ws), f"n={n}")
+
+
+def test_calls_on_another_stream_allocate_there():
+    side = torch.cuda.Stream()
+    args, kw = linear_inputs(9, 50, 256, (136, 64), 5, 16)
+    z, t = randn(gen(1), 4, 20000), tokens_for(gen(2), 4, 20000)
+    x, w = randn(gen(3), 6, 512).bfloat16(), torch.ones(512, device="cuda").bfloat16()
+    side.wait_stream(torch.cuda.current_stream())
+    y = step.lora_linear(*args, stream=side)
+    r = step.token_logprobs(z, t, 5, stream=side)
+    q = step.rms_norm(x, w, EPS, quant=True, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    check_linear(args, kw, y, "side stream")
+    check_score(z, t, 5, r)
+    check_norm(x, None, w, True, True, q)
+
+
+@pytest.mark.parametrize("n", [20, 700])
+def test_linear_graph_replays(n):
+    args, kw = linear_inputs(5, n, 512, (136, 64), 6, 16)
+    ws = step.linear_workspace(n, 512, 200, 2, 16)
+    out = step.lora_linear(*args, ws=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.lora_linear(*args, out=out, ws=ws)
+        step.lora_linear(*args, out=out, ws=ws)
+    for i in range(4):
+        args[0].copy_(randn(gen(40 + i), n, 512).bfloat16())
+        args[6].copy_(torch.randint(-1, 6, (n,), generator=gen(50 + i), device="cuda").int())
+        graph.replay()
+        torch.cuda.synchronize()
+        check_linear(args, kw, out, f"replay {i}")
+        assert torch.equal(out, step.lora_linear(*args, ws=ws))
