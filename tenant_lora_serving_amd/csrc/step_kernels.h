@@ -79,17 +79,15 @@ struct LinearArgs {
     uint16_t *y;
     int64_t ldy;
 };
-// How a projection runs: in small tiles of the rows as they come (at most
-// kUnsortedRows of them) or of the rows sorted by slot, or in large tiles of
-// the sorted rows.  The workspace holds the sorted rows' numbers and their
-// slots (row_words words each), then the inner sums.
-enum LinearPath { kRowsPath, kSortedRowsPath, kTiledPath };
+// Up to kUnsortedRows rows are taken as they come, more are sorted by slot
+// first.  The workspace holds the sorted rows' numbers and their slots
+// (row_words words each), then the inner sums.
 constexpr int kUnsortedRows = 256;
 struct LinearPlan {
-    LinearPath path;
+    bool sorted;
     size_t row_words, total_bytes;
 };
-LinearPlan linear_plan(int n, int k, int out, int num_slices, int R);
+LinearPlan linear_plan(int n, int num_slices, int R);
 struct LinearSpace {
     int32_t *perm, *key_of;
     uint16_t *xab;
@@ -101,6 +99,7 @@ inline LinearSpace linear_space(const LinearPlan &plan, void *ws) {
 hipError_t launch_lora_linear(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st);
 void launch_sort_rows(const LinearArgs &a, const LinearSpace &s, hipStream_t st);
 void launch_sorted_inner(const LinearArgs &a, const LinearSpace &s, hipStream_t st);
-void launch_lora_linear_tiled(const LinearArgs &a, const LinearSpace &s, hipStream_t st);
+void launch_lora_linear_tiled(const LinearArgs &a, const int32_t *perm, const int32_t *key_of, const uint16_t *xab,
+                              hipStream_t st);
 
 }  // namespace st

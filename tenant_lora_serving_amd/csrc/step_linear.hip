@@ -124,17 +124,113 @@ __global__ __launch_bounds__(kInThreads) void inner_kernel(LinearArgs a, uint16_
 }
 
 // ---------------------------------------------------------------- the product
-// SLOTS lines in a wave's ring.
 constexpr int kWaves = 4, kThreads = kWaves * kWave;
 struct Inner {
     const int32_t *perm, *key_of;  // sorted rows: their row numbers and slots
     const uint16_t *xab;
 };
+
+// The 8-bit form's scales: lane m holds row m's, columns from c0.
+template <int MT, int NT>
+__device__ __forceinline__ void apply_scales(const LinearArgs &a, float my_scale, int c0, int cols,
+                                             f32x4_t (&acc)[NT][MT]) {
+    const int lane = tl::lane_id();
+    float ws[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = 16 * j + 4 * (lane / 16) + e;
+            ws[j][e] = c < cols ? a.w_scale[c0 + c] : 0.0f;
+        }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const float xs = __shfl(my_scale, 16 * i + lane % 16);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][i][e] *= xs * ws[j][e];
+    }
+}
+
+// Adds xab B_s^T for the slots of the rows in `mine` to a wave's tile of rows
+// from m0 (lane m holds row m's slot) and columns c0 .. c0 + cols: slice by
+// slice, in steps of 32 of the 2 R terms of one slot (R rounded inner sums and
+// R rests, against the same B twice), kSteps steps on the way.
+constexpr int kSteps = 2;
+template <int MT, int NT>
+__device__ __forceinline__ void add_adapters(const LinearArgs &a, const uint16_t *xab, int out, int my_slot,
+                                             uint64_t mine, int m0, int c0, int cols, f32x4_t (&acc)[NT][MT],
+                                             int *any_broken) {
+    const int lane = tl::lane_id(), chunks = a.R / 8;
+    int first_slice = 0, end_slice = a.num_slices;
+    while (a.slice_off[first_slice + 1] <= c0) ++first_slice;
+    while (end_slice > first_slice + 1 && a.slice_off[end_slice - 1] >= c0 + cols) --end_slice;
+#pragma unroll 1
+    for (int slice = mine ? first_slice : end_slice; slice < end_slice; ++slice) {
+        const int lo = a.slice_off[slice] - c0, hi = min(a.slice_off[slice + 1] - c0, cols);
+        uint64_t todo = mine, same = 0;
+        int slot = -1, q0 = 0;
+        auto next_slot = [&]() {
+            q0 = 0;
+            slot = todo ? __builtin_amdgcn_readlane(my_slot, __builtin_ctzll(todo)) : -1;
+            same = slot >= 0 ? __ballot(my_slot == slot) : 0;
+            todo &= ~same;
+        };
+        u32x4_t bf[kSteps][NT], xf[kSteps][MT];
+        uint64_t who[kSteps];
+        auto load_steps = [&]() {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                who[s] = same;
+                const int q = q0 + lane / 16, r = (q >= chunks ? q - chunks : q) * 8;
+                const bool in = q < 2 * chunks && slot >= 0;
+                const uint16_t *B = a.b_pool + ((int64_t)slot * out + c0) * a.R + r;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int c = 16 * j + lane % 16;
+                    bf[s][j] = in && c >= lo && c < hi ? tl::ld16(B + (int64_t)c * a.R) : tl::zero4();
+                }
+                const uint16_t *X = xab + ((int64_t)m0 * a.num_slices + slice) * 2 * a.R + 8 * q;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const int m = 16 * i + lane % 16;
+                    xf[s][i] = in && (same >> m & 1) ? tl::ld16(X + (int64_t)m * a.num_slices * 2 * a.R) : tl::zero4();
+                }
+                if (slot >= 0 && (q0 += 4) >= 2 * chunks) next_slot();
+            }
+        };
+        next_slot();
+        load_steps();
+#pragma unroll 1
+        while (who[0]) {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                u16x2_t big = {};
+#pragma unroll
+                for (int j = 0; j < NT; ++j) big = larger_magnitude(big, bf[s][j]);
+                if (__ballot(not_finite(big))) {
+                    *any_broken = 1;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) drop_not_finite(bf[s][j]);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    if (!(who[s] >> (16 * i) & 0xffff)) continue;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) acc[j][i] = tl::mfma_16x16x32(bf[s][j], xf[s][i], acc[j][i]);
+                }
+            }
+            load_steps();
+        }
+    }
+}
+
+// SLOTS lines in a wave's ring.
 template <Form F, int MT, int NT, int SLOTS, bool SORTED>
 __global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, int out) {
     using Part = Partials<NT, MT>;
     using Ring = LineRing<NT, MT, SLOTS>;
-    constexpr int IT = 2;  // adapter steps on the way
     constexpr int kShared = Ring::kBytes > Part::kFloats * 4 ? Ring::kBytes : Part::kFloats * 4;
     __shared__ __align__(16) char shared[kWaves * kShared];
     float *red = reinterpret_cast<float *>(shared);  // over the rings, when they are done with
@@ -168,99 +264,18 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, i
     f32x4_t acc[NT][MT] = {};
     ring_product<F, NT, MT, SLOTS>(wr, wo, xr, xo, shared + wave * Ring::kBytes, wave, kWaves, lines, kbytes, acc);
 
-    if constexpr (FP8) {
-        const float my_scale = lane < rows ? a.x_scale[my_row] : 0.0f;
-        float ws[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = 16 * j + 4 * (lane / 16) + e;
-                ws[j][e] = c < cols ? a.w_scale[c0 + c] : 0.0f;
-            }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const float xs = __shfl(my_scale, 16 * i + lane % 16);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][i][e] *= xs * ws[j][e];
-        }
-    }
+    if constexpr (FP8) apply_scales(a, lane < rows ? a.x_scale[my_row] : 0.0f, c0, cols, acc);
 
-    // ---- the adapters, slice by slice, in steps of 32 of the 2 R terms of one
-    // slot (R rounded inner sums and R rests, against the same B twice), IT
-    // steps on the way.  A wave takes the slots that are its number modulo
-    // kWaves: so a row's sums meet in the same order whatever other rows share
-    // its tile, and the order of the sorted rows changes no result.
-    const int chunks = a.R / 8;
-    int first_slice = 0, end_slice = a.num_slices;
-    while (a.slice_off[first_slice + 1] <= c0) ++first_slice;
-    while (end_slice > first_slice + 1 && a.slice_off[end_slice - 1] >= c0 + cols) --end_slice;
-    const uint64_t with_slot = __ballot(my_slot >= 0), mine = __ballot(my_slot >= 0 && my_slot % kWaves == wave);
+    // A wave takes the adapters whose slot is its number modulo kWaves: so a
+    // row's sums meet in the same order whatever other rows share its tile, and
+    // the order of the sorted rows changes no result.
     int *any_broken = reinterpret_cast<int *>(shared + kWaves * kShared) - 1;  // past what is written below
     static_assert(kWaves * Part::kFloats * 4 <= kWaves * kShared - 4, "past the partial sums");
     __syncthreads();
     if (tid == 0) *any_broken = 0;
     __syncthreads();
-#pragma unroll 1
-    for (int slice = with_slot ? first_slice : end_slice; slice < end_slice; ++slice) {
-        const int lo = a.slice_off[slice] - c0, hi = min(a.slice_off[slice + 1] - c0, cols);
-        uint64_t todo = mine, same = 0;
-        int slot = -1, q0 = 0;
-        auto next_slot = [&]() {
-            q0 = 0;
-            slot = todo ? __builtin_amdgcn_readlane(my_slot, __builtin_ctzll(todo)) : -1;
-            same = slot >= 0 ? __ballot(my_slot == slot) : 0;
-            todo &= ~same;
-        };
-        u32x4_t bf[IT][NT], xf[IT][MT];
-        uint64_t who[IT];
-        auto load_steps = [&]() {
-#pragma unroll
-            for (int s = 0; s < IT; ++s) {
-                who[s] = same;
-                const int q = q0 + lane / 16, r = (q >= chunks ? q - chunks : q) * 8;
-                const bool in = q < 2 * chunks && slot >= 0;
-                const uint16_t *B = a.b_pool + ((int64_t)slot * out + c0) * a.R + r;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int c = 16 * j + lane % 16;
-                    bf[s][j] = in && c >= lo && c < hi ? tl::ld16(B + (int64_t)c * a.R) : tl::zero4();
-                }
-                const uint16_t *X = h.xab + ((int64_t)m0 * a.num_slices + slice) * 2 * a.R + 8 * q;
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const int m = 16 * i + lane % 16;
-                    xf[s][i] = in && (same >> m & 1) ? tl::ld16(X + (int64_t)m * a.num_slices * 2 * a.R) : tl::zero4();
-                }
-                if (slot >= 0 && (q0 += 4) >= 2 * chunks) next_slot();
-            }
-        };
-        next_slot();
-        load_steps();
-#pragma unroll 1
-        while (who[0]) {
-#pragma unroll
-            for (int s = 0; s < IT; ++s) {
-                u16x2_t big = {};
-#pragma unroll
-                for (int j = 0; j < NT; ++j) big = larger_magnitude(big, bf[s][j]);
-                if (__ballot(not_finite(big))) {
-                    *any_broken = 1;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) drop_not_finite(bf[s][j]);
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    if (!(who[s] >> (16 * i) & 0xffff)) continue;
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[j][i] = tl::mfma_16x16x32(bf[s][j], xf[s][i], acc[j][i]);
-                }
-            }
-            load_steps();
-        }
-    }
+    add_adapters<MT, NT>(a, h.xab, out, my_slot, __ballot(my_slot >= 0 && my_slot % kWaves == wave), m0, c0, cols, acc,
+                         any_broken);
 
     __syncthreads();
     Part::put(red, wave, acc);
@@ -277,6 +292,124 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, i
         mark_broken<kThreads>(a, out, m0, rows, c0, cols, SORTED ? h.perm : nullptr, SORTED ? h.key_of : a.slot);
 }
 
+// ---------------------------------------------------------------- middling products
+// 128 sorted rows x 128 columns by four waves, 64 x 64 each, for products that
+// 256 x 256 tiles would not spread over the chip and 64 x 64 tiles read too
+// often.  Lines go through kMidSlots buffers of LDS that the waves share; a
+// wave multiplies a line from registers while it reads the next one's
+// fragments, two matrix instructions to a read, and the loads of two more
+// lines are out: a line keeps the matrix cores and the LDS busy for 512 and
+// 768 cycles.
+constexpr int kMidTile = 128, kMidSlots = 4, kMidLoads = 8, kMidSlot = 2 * kMidTile * kLine;
+template <Form F>
+__global__ __launch_bounds__(kThreads) void mid_kernel(LinearArgs a, Inner h, int out) {
+    __shared__ __align__(16) char lds[kMidSlots * kMidSlot];
+    const int lane = tl::lane_id(), tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
+    // row tiles of the same columns run next to each other on one XCD
+    const int m_tiles = (a.n + kMidTile - 1) / kMidTile, on_xcd = blockIdx.x / 8;
+    const int c0 = (on_xcd / m_tiles * 8 + blockIdx.x % 8) * kMidTile, m0 = on_xcd % m_tiles * kMidTile;
+    if (c0 >= out) return;
+    const int rows = min(a.n - m0, kMidTile), cols = min(out - c0, kMidTile);
+    constexpr int esz = F == kBf16 ? 2 : 1;
+    const int kbytes = a.k * esz, lines = (kbytes + kLine - 1) / kLine;
+    const int64_t ldx = F == kBf16 ? a.ldx * 2 : a.ldxq;
+
+    // Waves 0 and 1 load the rows of x, 2 and 3 those of w, 8 rows an
+    // instruction; LDS place c of row r holds chunk c ^ (r % 8).
+    const int l8 = lane / 8, chunk = ((lane & 7) ^ l8) * 16, half = wave % 2 * 64;
+    const i32x4_t rsrc = wave < 2 ? words_rsrc(F == kBf16 ? (const void *)a.x : (const void *)a.xq,
+                                               (uint32_t)((int64_t)(a.n - 1) * ldx + kbytes))
+                                  : words_rsrc((const char *)a.w + (int64_t)c0 * kbytes, (uint32_t)(cols * kbytes));
+    uint32_t off[kMidLoads];
+#pragma unroll
+    for (int u = 0; u < kMidLoads; ++u) {
+        const int r = half + 8 * u + l8;
+        off[u] = wave < 2 ? (r < rows ? (uint32_t)((int64_t)h.perm[m0 + r] * ldx) : kOob)
+                          : (r < cols ? (uint32_t)(r * kbytes) : kOob);
+    }
+    const uint32_t to = lds_address(lds) + wave * (kMidSlot / kWaves);
+    auto start = [&](int slot, int line) __attribute__((always_inline)) {
+        const int at = line * kLine + chunk;
+        const uint32_t o = at < kbytes ? (uint32_t)at : kOob;
+#pragma unroll
+        for (int u = 0; u < kMidLoads; ++u) load_lds(rsrc, off[u] + o, 0, to + slot * kMidSlot + u * 1024);
+    };
+    const int wm = wave % 2 * 64, wn = wave / 2 * 64;
+    const int rd = (lane % 16) * kLine + (((lane / 16) ^ (lane & 7)) * 16);
+    Line x[2][4], w[2][4];
+    auto read = [&](int into, int slot) __attribute__((always_inline)) {
+        const char *p = lds + slot * kMidSlot;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const char *q = p + (wm + 16 * i) * kLine;
+            x[into][i] = Line{tl::ld16(q + rd), tl::ld16(q + (rd ^ 64))};
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const char *q = p + (kMidTile + wn + 16 * j) * kLine;
+            w[into][j] = Line{tl::ld16(q + rd), tl::ld16(q + (rd ^ 64))};
+        }
+    };
+    f32x4_t acc[4][4] = {};
+#pragma unroll
+    for (int d = 0; d < kMidSlots - 1; ++d) start(d, d);
+    wait_loads<(kMidSlots - 2) * kMidLoads>();
+    barrier();
+    read(0, 0);
+#pragma unroll 1
+    for (int t = 0; t < lines; t += kMidSlots) {
+#pragma unroll
+        for (int d = 0; d < kMidSlots; ++d) {
+            // line t + d + 1 has arrived, and nobody reads line t + d - 1 any more
+            wait_loads<(kMidSlots - 3) * kMidLoads>();
+            barrier();
+            start((d + kMidSlots - 1) % kMidSlots, t + d + kMidSlots - 1);
+            read((d + 1) % 2, (d + 1) % kMidSlots);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] = mma_line<F>(w[d % 2][j], x[d % 2][i], acc[j][i]);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                // a read of LDS,
+                __builtin_amdgcn_sched_group_barrier(0x008, F == kBf16 ? 2 : 1, 0);  // then matrix instructions
+            }
+        }
+    }
+    wait_loads<0>();  // (lines past the end still write zeros)
+    int &any_broken = *reinterpret_cast<int *>(lds);
+    __syncthreads();
+    if (tid == 0) any_broken = 0;
+    __syncthreads();
+
+    // ---- this wave's 64 x 64
+    const int m1 = m0 + wm, c1 = c0 + wn, my_rows = rows - wm, my_cols = min(cols - wn, 64);
+    const bool here = lane < my_rows;
+    const int my_row = here ? h.perm[m1 + lane] : 0, key = here ? h.key_of[m1 + lane] : a.num_slots;
+    const int my_slot = key < a.num_slots ? key : -1;
+    if (my_rows > 0 && my_cols > 0) {
+        if constexpr (F != kBf16) apply_scales(a, here ? a.x_scale[my_row] : 0.0f, c1, my_cols, acc);
+        add_adapters<4, 4>(a, h.xab, out, my_slot, __ballot(my_slot >= 0), m1, c1, my_cols, acc, &any_broken);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = 16 * i + lane % 16, r = __shfl(my_row, m);
+            if (m >= my_rows) continue;
+            uint16_t *y = a.y + (int64_t)r * a.ldy + c1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = 16 * j + 4 * (lane / 16);
+                if (c < my_cols)
+                    *reinterpret_cast<uint2 *>(y + c) = make_uint2(tl::pack_bf16x2(acc[j][i][0], acc[j][i][1]),
+                                                                   tl::pack_bf16x2(acc[j][i][2], acc[j][i][3]));
+            }
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // before another thread may write a result again
+    __syncthreads();
+    if (any_broken) mark_broken<kThreads>(a, out, m0, rows, c0, cols, h.perm, h.key_of);
+}
+
 template <Form F, int MT, int NT, int SLOTS>
 void go(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
     const int m_tiles = (a.n + 16 * MT - 1) / (16 * MT), c_tiles = (out + 16 * NT - 1) / (16 * NT);
@@ -291,14 +424,40 @@ void go(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
 }
 
 template <Form F>
+void go_mid(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
+    const int m_tiles = (a.n + kMidTile - 1) / kMidTile, c_tiles = (out + kMidTile - 1) / kMidTile;
+    mid_kernel<F><<<dim3((unsigned)((c_tiles + 7) / 8 * 8) * m_tiles), kThreads, 0, st>>>(a, h, out);
+}
+
+long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// Microseconds of a product of `tiles` tiles, one a CU at a time: `fixed` and
+// `line` those of a tile and of a line of its k.
+double rounds_us(long long tiles, double fixed, double line, double lines) {
+    return 8.0 + (double)cdiv(tiles, 256) * (fixed + line * lines);
+}
+
+template <Form F>
 void pick(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
     const int tiles = (out + 15) / 16;
     if (a.n <= 16) return tiles > 768 ? go<F, 1, 2, 3>(a, h, out, st) : go<F, 1, 1, 4>(a, h, out, st);
     if (a.n <= 32) return tiles > 768 ? go<F, 2, 4, 2>(a, h, out, st) : go<F, 2, 1, 4>(a, h, out, st);
-    const int m_tiles = (a.n + 63) / 64;
-    auto rounds = [&](int nt) { return ((tiles + nt - 1) / nt * m_tiles + 255) / 256 * (4 + nt + 3); };
-    if (rounds(6) <= rounds(4) && rounds(6) <= rounds(2)) return go<F, 4, 6, 2>(a, h, out, st);
-    return rounds(4) <= rounds(2) ? go<F, 4, 4, 2>(a, h, out, st) : go<F, 4, 2, 3>(a, h, out, st);
+    // the times below were fitted to single products (k 1008 to 4096)
+    const double lines = (double)cdiv((long long)a.k * (F == kBf16 ? 2 : 1), kLine);
+    auto small = [&](int nt) {
+        return rounds_us(cdiv(tiles, nt) * cdiv(a.n, 64), 4.0, 0.11 * (4 + nt), (double)cdiv((long long)lines, kWaves));
+    };
+    const double s2 = small(2), s4 = small(4), s6 = small(6), best = s2 < s4 ? (s2 < s6 ? s2 : s6) : (s4 < s6 ? s4 : s6);
+    if constexpr (F != kE4m3AsBf16) {
+        if (h.perm) {
+            const double mid = rounds_us(cdiv(out, kMidTile) * cdiv(a.n, kMidTile), 4.0, 0.58, lines);
+            const double large = rounds_us(cdiv(out, 256) * cdiv(a.n, 256), 8.0, F == kBf16 ? 1.6 : 1.8, lines);
+            if (large <= mid && large <= best) return launch_lora_linear_tiled(a, h.perm, h.key_of, h.xab, st);
+            if (mid <= best) return go_mid<F>(a, h, out, st);
+        }
+    }
+    if (s6 <= best) return go<F, 4, 6, 2>(a, h, out, st);
+    return s4 <= best ? go<F, 4, 4, 2>(a, h, out, st) : go<F, 4, 2, 3>(a, h, out, st);
 }
 
 }  // namespace
@@ -306,21 +465,19 @@ void pick(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
 hipError_t launch_lora_linear(const LinearArgs &a, const LinearPlan &plan, void *ws, hipStream_t st) {
     const int out = a.slice_off[a.num_slices];
     const LinearSpace s = linear_space(plan, ws);
-    if (plan.path != kRowsPath) launch_sort_rows(a, s, st);
-    if (plan.path != kRowsPath) {
+    if (plan.sorted) {
+        launch_sort_rows(a, s, st);
         launch_sorted_inner(a, s, st);
     } else {
         // groups of up to 16 rows of one slot: every slot ends one that is not full
         const int most = a.n / 16 + a.num_slots, groups = a.n < most ? a.n : most, LR = a.num_slices * a.R;
-        if (groups * ((LR + 15) / 16) <= 512) inner_kernel<1, 4><<<dim3(groups, (LR + 15) / 16), kInThreads, 0, st>>>(a, s.xab);
-        else inner_kernel<4, 2><<<dim3(groups, (LR + 63) / 64), kInThreads, 0, st>>>(a, s.xab);
+        // (1168 units of 16 columns took 83 us where 236 of 64 take 50)
+        if (groups * ((LR + 15) / 16) <= 512)
+            inner_kernel<1, 4><<<dim3(groups, (LR + 15) / 16), kInThreads, 0, st>>>(a, s.xab);
+        else
+            inner_kernel<4, 2><<<dim3(groups, (LR + 63) / 64), kInThreads, 0, st>>>(a, s.xab);
     }
-    if (plan.path == kTiledPath) {
-        launch_lora_linear_tiled(a, s, st);
-        return hipGetLastError();
-    }
-    const bool sorted = plan.path == kSortedRowsPath;
-    const Inner h{sorted ? s.perm : nullptr, s.key_of, s.xab};
+    const Inner h{plan.sorted ? s.perm : nullptr, s.key_of, s.xab};
     if (a.xq && a.k <= kExactK) pick<kE4m3AsBf16>(a, h, out, st);
     else if (a.xq) pick<kE4m3>(a, h, out, st);
     else pick<kBf16>(a, h, out, st);

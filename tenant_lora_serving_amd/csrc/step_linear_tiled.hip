@@ -65,15 +65,18 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const int32_t *slot,
 }
 
 // ---------------------------------------------------------------- inner sums
-// scale[s] x A_s^T for 32 sorted rows and 64 of the num_slices * R rows of
-// A_s, for each gridDim.z-th slot that the rows name; written as [row][slice][R rounded
-// values, R rests] in bf16.  Four waves take every fourth line of k.
-constexpr int kInMT = 2, kInNT = 4, kInSlots = 2, kInRows = 16 * kInMT, kInCols = 16 * kInNT;
-__global__ __launch_bounds__(256) void sorted_inner_kernel(LinearArgs a, const int32_t *perm, const int32_t *key_of,
+// scale[s] x A_s^T for 32 sorted rows and 16 NT of the num_slices * R rows
+// of A_s, for each gridDim.z-th slot that the rows name; written as [row][slice][R rounded
+// values, R rests] in bf16.  The waves take
+// every WAVES-th line of k.
+constexpr int kInMT = 2, kInRows = 16 * kInMT;
+template <int kInNT, int kInSlots, int WAVES>
+__global__ __launch_bounds__(WAVES *kWave) void sorted_inner_kernel(LinearArgs a, const int32_t *perm, const int32_t *key_of,
                                                            uint16_t *xab) {
+    constexpr int kInCols = 16 * kInNT, kThreads = WAVES * kWave;
     using Part = Partials<kInNT, kInMT>;
     using Ring = LineRing<kInNT, kInMT, kInSlots>;
-    __shared__ __align__(16) char shared[4 * Ring::kBytes > 4 * Part::kFloats * 4 ? 4 * Ring::kBytes : 4 * Part::kFloats * 4];
+    __shared__ __align__(16) char shared[WAVES * (Ring::kBytes > Part::kFloats * 4 ? Ring::kBytes : Part::kFloats * 4)];
     float *red = reinterpret_cast<float *>(shared);
     const int lane = tl::lane_id(), tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
     char *ring = shared + wave * Ring::kBytes;
@@ -101,16 +104,16 @@ __global__ __launch_bounds__(256) void sorted_inner_kernel(LinearArgs a, const i
             xo[u] = same >> m & 1 ? (uint32_t)((int64_t)row * a.ldx * 2) : kOob;
         }
         f32x4_t acc[kInNT][kInMT] = {};
-        ring_product<kBf16, kInNT, kInMT, kInSlots>(wr, wo, xr, xo, ring, wave, 4, lines, kbytes, acc);
+        ring_product<kBf16, kInNT, kInMT, kInSlots>(wr, wo, xr, xo, ring, wave, WAVES, lines, kbytes, acc);
         __syncthreads();  // (the partial sums lie over the rings)
         Part::put(red, wave, acc);
         __syncthreads();
         const float scale = a.scale[slot];
-        for (int t = tid; t < kInRows * kInCols / 8; t += 256) {
+        for (int t = tid; t < kInRows * kInCols / 8; t += kThreads) {
             const int m = t / (kInCols / 8), c = t % (kInCols / 8) * 8;
             if (!(same >> m & 1) || c0 + c >= LR) continue;
             float v[8];
-            Part::sum8<4>(red, m, c, v);
+            Part::template sum8<WAVES>(red, m, c, v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= scale;
             put_inner8(xab, p0 + m, c0 + c, a.num_slices, a.R, v);
@@ -446,18 +449,22 @@ void launch_sort_rows(const LinearArgs &a, const LinearSpace &s, hipStream_t st)
 }
 
 void launch_sorted_inner(const LinearArgs &a, const LinearSpace &s, hipStream_t st) {
-    const int tiles = (a.n + kInRows - 1) / kInRows, cols = (a.num_slices * a.R + kInCols - 1) / kInCols;
+    const int tiles = (a.n + kInRows - 1) / kInRows, LR = a.num_slices * a.R, wide = (LR + 63) / 64;
     // 32 rows name 1 + S / tiles slots on average where all S are named alike;
     // one workgroup for all of them took 95 us for 300 rows of 300 slots
-    const int split = 1 + a.num_slots / tiles;
-    sorted_inner_kernel<<<dim3(tiles, cols, split < kInRows ? split : kInRows), 256, 0, st>>>(a, s.perm, s.key_of,
-                                                                                              s.xab);
+    const int named = 1 + a.num_slots / tiles, split = named < kInRows ? named : kInRows;
+    // columns of 64 read x less often; with few of them the CUs that idle cost more
+    if (tiles * wide * split >= 256)
+        sorted_inner_kernel<4, 2, 4><<<dim3(tiles, wide, split), 256, 0, st>>>(a, s.perm, s.key_of, s.xab);
+    else
+        sorted_inner_kernel<1, 3, 8><<<dim3(tiles, (LR + 15) / 16, split), 512, 0, st>>>(a, s.perm, s.key_of, s.xab);
 }
 
-void launch_lora_linear_tiled(const LinearArgs &a, const LinearSpace &s, hipStream_t st) {
+void launch_lora_linear_tiled(const LinearArgs &a, const int32_t *perm, const int32_t *key_of, const uint16_t *xab,
+                              hipStream_t st) {
     const int out = a.slice_off[a.num_slices];
-    if (a.xq) go<kE4m3>(a, s.perm, s.key_of, s.xab, out, st);
-    else go<kBf16>(a, s.perm, s.key_of, s.xab, out, st);
+    if (a.xq) go<kE4m3>(a, perm, key_of, xab, out, st);
+    else go<kBf16>(a, perm, key_of, xab, out, st);
 }
 
 }  // namespace st

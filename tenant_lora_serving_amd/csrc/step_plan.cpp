@@ -32,12 +32,11 @@ ScorePlan score_plan(int n, int v, int top, int fp32) {
     return p;
 }
 
-LinearPlan linear_plan(int n, int k, int out, int num_slices, int R) {
+LinearPlan linear_plan(int n, int num_slices, int R) {
     LinearPlan p{};
-    (void)out;
-    p.path = n > 1024 && k > kExactK ? kTiledPath : n > kUnsortedRows ? kSortedRowsPath : kRowsPath;
+    p.sorted = n > kUnsortedRows;
     const size_t inner = (size_t)n * num_slices * R * 2 * sizeof(uint16_t);
-    if (p.path != kRowsPath) p.row_words = up256((size_t)n * sizeof(int32_t)) / sizeof(int32_t);
+    if (p.sorted) p.row_words = up256((size_t)n * sizeof(int32_t)) / sizeof(int32_t);
     p.total_bytes = 2 * p.row_words * sizeof(int32_t) + up256(inner);
     return p;
 }

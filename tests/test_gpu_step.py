@@ -500,3 +500,29 @@ def test_linear_graph_replays(n):
         torch.cuda.synchronize()
         check_linear(args, kw, out, f"replay {i}")
         assert torch.equal(out, step.lora_linear(*args, ws=ws))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,k,widths,S,R", [
+    (1000, 2064, (2000, 1008), 20, 24), (700, 1040, (4104,), 700, 8), (257, 4096, (8, 8184), 3, 128),
+    (513, 528, (7176, 1000), 40, 16), (900, 1552, (1536, 1536, 1528), 2, 64), (384, 272, (16392,), 5, 32),
+])
+def test_linear_middling(n, k, widths, S, R, fp8):
+    print(f"linear middling n={n} k={k} widths={widths} S={S} R={R} fp8={fp8}", flush=True)
+    args, kw = linear_inputs(n + k, n, k, widths, S, R, fp8, pad=16 if n % 2 else 0)
+    check_linear(args, kw, step.lora_linear(*args, **kw), "linear")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_linear_middling_broken_adapter(fp8):
+    n, widths, k = 600, (4000, 2008), 1040
+    args, kw = linear_inputs(3, n, k, widths, 7, 16, fp8, slot=torch.arange(n, device="cuda") % 7)
+    x, w, a, b, scale, _, slot = args
+    y, tol = linear64(args, kw)
+    b = b.clone()
+    b[2, 7, 3], b[4, 5000, 0] = math.nan, math.inf
+    at = torch.arange(sum(widths), device="cuda")[None, :]
+    broken = (slot == 2)[:, None] & (at == 7) | (slot == 4)[:, None] & (at == 5000)
+    got = step.lora_linear(x, w, a, b, scale, widths, slot, **kw)
+    assert not got[broken].isfinite().any()
+    within(got[~broken], y[~broken], tol[~broken], "the others")
