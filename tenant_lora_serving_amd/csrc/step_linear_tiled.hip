@@ -45,7 +45,19 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const int32_t *slot,
         const int s = slot[r];
         return s >= 0 && s < S ? s : S;
     };
-    for (int r = tid; r < n; r += kSortThreads) atomicAdd(&place[key_at(r)], 1);
+    // Adds 1 to the row's slot's word; its value before is the answer.  A wave
+    // whose rows are all of one slot, as in a long prompt, adds once (64 lanes
+    // on one word take their turns: 14 us for 6947 rows).
+    auto count = [&](int key) {
+        const uint64_t here = __ballot(true);
+        const int first = __builtin_amdgcn_readfirstlane(key);
+        if (__ballot(key == first) != here) return atomicAdd(&place[key], 1);
+        const int rank = __popcll(here & tl::lanemask_lt());
+        int before = 0;
+        if (rank == 0) before = atomicAdd(&place[first], __popcll(here));
+        return __builtin_amdgcn_readfirstlane(before) + rank;
+    };
+    for (int r = tid; r < n; r += kSortThreads) count(key_at(r));
     __syncthreads();
     const int per = (S + kSortThreads) / kSortThreads, s0 = min(tid * per, S + 1), s1 = min(s0 + per, S + 1);
     int mine = 0, total;
@@ -58,7 +70,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const int32_t *slot,
     }
     __syncthreads();
     for (int r = tid; r < n; r += kSortThreads) {
-        const int key = key_at(r), p = atomicAdd(&place[key], 1);
+        const int key = key_at(r), p = count(key);
         perm[p] = r;
         key_of[p] = key;
     }
@@ -80,7 +92,15 @@ __global__ __launch_bounds__(WAVES *kWave) void sorted_inner_kernel(LinearArgs a
     float *red = reinterpret_cast<float *>(shared);
     const int lane = tl::lane_id(), tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
     char *ring = shared + wave * Ring::kBytes;
-    const int p0 = blockIdx.x * kInRows, c0 = blockIdx.y * kInCols, LR = a.num_slices * a.R;
+    // Of many tiles an XCD takes a run of row tiles, all columns of each: they
+    // share rows of x and, mostly, the adapter in its L2 (48 -> 43 us for 6947
+    // rows).  A few are spread over all XCDs.
+    const int LR = a.num_slices * a.R, c_tiles = (LR + kInCols - 1) / kInCols;
+    const int on_xcd = blockIdx.x / 8, per_xcd = gridDim.x / 8 / c_tiles;
+    const bool runs = per_xcd >= 8;
+    const int tile = runs ? blockIdx.x % 8 * per_xcd + on_xcd / c_tiles : (int)blockIdx.x / c_tiles;
+    const int p0 = tile * kInRows, c0 = (runs ? on_xcd : (int)blockIdx.x) % c_tiles * kInCols;
+    if (p0 >= a.n) return;
     const int kbytes = a.k * 2, lines = (kbytes + kLine - 1) / kLine;
     const i32x4_t xr = words_rsrc(a.x, (uint32_t)(((int64_t)(a.n - 1) * a.ldx + a.k) * 2));
     const bool here = lane < kInRows && p0 + lane < a.n;
@@ -453,11 +473,13 @@ void launch_sorted_inner(const LinearArgs &a, const LinearSpace &s, hipStream_t 
     // 32 rows name 1 + S / tiles slots on average where all S are named alike;
     // one workgroup for all of them took 95 us for 300 rows of 300 slots
     const int named = 1 + a.num_slots / tiles, split = named < kInRows ? named : kInRows;
+    const unsigned all = (tiles + 7) / 8 * 8;
     // columns of 64 read x less often; with few of them the CUs that idle cost more
     if (tiles * wide * split >= 256)
-        sorted_inner_kernel<4, 2, 4><<<dim3(tiles, wide, split), 256, 0, st>>>(a, s.perm, s.key_of, s.xab);
+        sorted_inner_kernel<4, 2, 4><<<dim3(all * wide, 1, split), 256, 0, st>>>(a, s.perm, s.key_of, s.xab);
     else
-        sorted_inner_kernel<1, 3, 8><<<dim3(tiles, (LR + 15) / 16, split), 512, 0, st>>>(a, s.perm, s.key_of, s.xab);
+        sorted_inner_kernel<1, 3, 8>
+            <<<dim3(all * ((LR + 15) / 16), 1, split), 512, 0, st>>>(a, s.perm, s.key_of, s.xab);
 }
 
 void launch_lora_linear_tiled(const LinearArgs &a, const int32_t *perm, const int32_t *key_of, const uint16_t *xab,

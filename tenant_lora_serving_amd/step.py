@@ -85,12 +85,13 @@ def _rows(t: torch.Tensor, name: str, *dtypes) -> tuple:
 
 def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int):
     """A contiguous tensor of this type and shape on device `dev`: its pointer."""
-    p = _dev(t, name, dtype)
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _dev(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on another device")
-    return p
+    raise ValueError(f"{name} is on another device")
 
 
 def _same(name: str, got, want):
@@ -136,14 +137,14 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, *, residu
         rp, ldr = _rows(residual, "residual", torch.bfloat16)
         _same("residual", residual.shape, (n, h))
         if residual_out is None:
-            residual_out = x.new_empty((n, h))
+            residual_out = torch.empty_like(x)
         sp = _arg(residual_out, "residual_out", torch.bfloat16, (n, h), dev)
         if sp == rp:
             ldr = h if n <= 1 else ldr
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    y = x.new_empty((n, h)) if bf16 else None
-    q = x.new_empty((n, h), dtype=torch.float8_e4m3fn) if quant else None
+    y = torch.empty_like(x) if bf16 else None
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn) if quant else None
     q_scale = x.new_empty(n, dtype=torch.float32) if quant else None
     st = lib().step_rms_norm(xp, ldx, rp, ldr, wp, n, h, eps, sp, y.data_ptr() if bf16 else None,
                              q.data_ptr() if quant else None, q_scale.data_ptr() if quant else None, _raw_stream(dev))
@@ -243,8 +244,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, *, 
     n, v = logits.shape
     dev = _device(logits, ws)
     tp = _arg(tokens, "tokens", torch.int32, (n,), dev)
-    logprob, rank = tokens.new_empty(n, dtype=torch.float32), tokens.new_empty(n)
-    entropy = tokens.new_empty(n, dtype=torch.float32)
+    logprob, rank = torch.empty_like(tokens, dtype=torch.float32), torch.empty_like(tokens)
+    entropy = torch.empty_like(logprob)
     ids = best = ip = bp = None
     if top > 0:
         ids, best = tokens.new_empty((n, top)), tokens.new_empty((n, top), dtype=torch.float32)
