@@ -31,6 +31,7 @@ hipError_t launch_rms_norm(const NormArgs &a, hipStream_t st);
 // A row of logits is cut into `parts` pieces, one workgroup each; the last
 // workgroup of a row to finish joins them.
 constexpr int kScoreThreads = 512;
+constexpr int kScoreShortThreads = 128;  // for many short rows, one piece each
 constexpr int kScoreLaneElems = 64;  // logits per thread of a piece at most
 constexpr int kScoreMaxParts = 64;
 // The tickets (a word a row, 0 between calls) have a place of their own, the
@@ -40,6 +41,7 @@ constexpr int kScoreMaxRows = 1 << 16;
 // count, then `top` 64-bit keys as (high, low).
 __host__ __device__ inline int score_record_words(int top) { return 4 + 2 * top; }
 struct ScorePlan {
+    int threads;          // of a workgroup
     int parts, part_ids;  // pieces of a row, 16-byte vectors of a piece
     size_t ticket_bytes, total_bytes;
 };

@@ -17,12 +17,22 @@ long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 ScorePlan score_plan(int n, int v, int top, int fp32) {
     const int E = fp32 ? 4 : 8;
     const long long ids = v / E + 2;  // whole vectors and the two ragged ends
+    ScorePlan p{};
+    // enough rows to fill the chip, and each within eight vectors of 128
+    // threads: 2000 rows of 1417 floats, top 1: 10 us; with 512
+    // threads a row, most of them idle in every selection, 22 us
+    if (n >= 256 && ids <= 8 * kScoreShortThreads) {
+        p.threads = kScoreShortThreads;
+        p.parts = 1;
+        p.part_ids = (int)ids;
+        return p;
+    }
+    p.threads = kScoreThreads;
     const long long least = cdiv(ids, (long long)kScoreThreads * (kScoreLaneElems / E));
     long long parts = cdiv(512, n > 0 ? n : 1);
     if (parts > cdiv(ids, kScoreThreads)) parts = cdiv(ids, kScoreThreads);
     if (parts > kScoreMaxParts) parts = kScoreMaxParts;
     if (parts < least) parts = least;
-    ScorePlan p{};
     p.part_ids = (int)cdiv(ids, parts);
     p.parts = (int)cdiv(ids, p.part_ids);
     if (p.parts > 1) {

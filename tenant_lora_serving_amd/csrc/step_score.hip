@@ -29,8 +29,6 @@ using tl::u32x4_t;
 
 namespace {
 
-constexpr int kThreads = kScoreThreads;
-constexpr int kGroup = kThreads / kWave;  // threads per group of the first selection: 64 groups
 constexpr int kCandidates = kMaxTop * kScoreLaneElems;
 constexpr int kUnroll = 4;
 static_assert(kScoreMaxParts <= kWave && kMaxTop * kMaxTop <= kCandidates, "one wave joins a row's parts");
@@ -163,22 +161,26 @@ __device__ __forceinline__ uint64_t kth_of_64(const uint64_t *keys, int k) {
     return keys[__builtin_ctzll(hit)];
 }
 
+// T threads a workgroup: T / 64 threads per group of the first selection, so
+// 64 groups.
+template <int T>
 struct Shared {
+    static constexpr int kGroup = T / kWave;
     uint64_t groups[kWave];
     uint64_t lanes[kMaxTop * kGroup];  // thread maxima at or above the first bound
     int owner[kMaxTop * kGroup];
     int sel[kMaxTop];
     uint64_t cand[kCandidates];
-    Stat stats[kThreads / kWave];
+    Stat stats[T / kWave];
     uint64_t bound;
     int n_lanes, n_cand, last;
 };
 
 // Ranks the collected candidates and hands each of the first k to `put`.
-template <class Put>
-__device__ __forceinline__ void rank_candidates(const Shared &sh, int k, Put put) {
+template <int T, class Put>
+__device__ __forceinline__ void rank_candidates(const Shared<T> &sh, int k, Put put) {
     const int n = sh.n_cand;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
+    for (int i = threadIdx.x; i < n; i += T) {
         const uint64_t mine = sh.cand[i];
         int rank = 0;
         for (int j = 0; j < n; ++j) rank += sh.cand[j] > mine ? 1 : 0;
@@ -186,8 +188,9 @@ __device__ __forceinline__ void rank_candidates(const Shared &sh, int k, Put put
     }
 }
 
-template <bool F32>
-__device__ __forceinline__ void part_top(const Row<F32> &r, const Lane &a, int id0, int id1, int k, Shared &sh) {
+template <bool F32, int T>
+__device__ __forceinline__ void part_top(const Row<F32> &r, const Lane &a, int id0, int id1, int k, Shared<T> &sh) {
+    constexpr int kGroup = Shared<T>::kGroup;
     constexpr int E = Row<F32>::E;
     const int tid = threadIdx.x;
     const uint64_t mine = make_key(a.m, a.best < 0 ? 0 : r.start(a.best));
@@ -220,9 +223,9 @@ __device__ __forceinline__ void part_top(const Row<F32> &r, const Lane &a, int i
     }
     __syncthreads();
     const uint64_t bound = sh.bound;
-    const int nsel = nl < k ? nl : k, per = (id1 - id0 + kThreads - 1) / kThreads;
-    for (int i = tid; i < nsel * per; i += kThreads) {
-        const int id = id0 + sh.sel[i / per] + (i % per) * kThreads;
+    const int nsel = nl < k ? nl : k, per = (id1 - id0 + T - 1) / T;
+    for (int i = tid; i < nsel * per; i += T) {
+        const int id = id0 + sh.sel[i / per] + (i % per) * T;
         if (id >= id1) continue;
         float z[E];
         r.load(id, z);
@@ -268,11 +271,11 @@ __device__ __forceinline__ void st_agent(uint32_t *p, uint32_t v) {
     __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a, int parts, int part_ids, int32_t *tickets,
+template <bool F32, int T>
+__global__ __launch_bounds__(T) void score_kernel(ScoreArgs a, int parts, int part_ids, int32_t *tickets,
                                                          uint32_t *records) {
     constexpr int E = Row<F32>::E;
-    __shared__ Shared sh;
+    __shared__ Shared<T> sh;
     const int tid = threadIdx.x, k = a.top;
     const int row = blockIdx.x / parts, part = blockIdx.x % parts;
     const Row<F32> r(a.logits, a.ld, row, a.v);
@@ -283,19 +286,19 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a, int parts,
 
     // ---- the pass over this part's logits
     Lane s{-INFINITY, 0.0f, 0.0f, 0, -1};
-    for (int id = id0 + tid; id < id1; id += kUnroll * kThreads) {
+    for (int id = id0 + tid; id < id1; id += kUnroll * T) {
         float z[kUnroll][E];
-        if (id >= 1 && id + (kUnroll - 1) * kThreads < id1 && id + (kUnroll - 1) * kThreads <= r.nvec) {
+        if (id >= 1 && id + (kUnroll - 1) * T < id1 && id + (kUnroll - 1) * T <= r.nvec) {
             u32x4_t w[kUnroll];
 #pragma unroll
-            for (int j = 0; j < kUnroll; ++j) w[j] = tl::ld16(r.vec(id + j * kThreads));
+            for (int j = 0; j < kUnroll; ++j) w[j] = tl::ld16(r.vec(id + j * T));
 #pragma unroll
             for (int j = 0; j < kUnroll; ++j) Row<F32>::unpack(w[j], z[j]);
         } else {
 #pragma unroll
             for (int j = 0; j < kUnroll; ++j) {
-                if (id + j * kThreads < id1) {
-                    r.load(id + j * kThreads, z[j]);
+                if (id + j * T < id1) {
+                    r.load(id + j * T, z[j]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < E; ++i) z[j][i] = -INFINITY;
@@ -308,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a, int parts,
         if (all > s.m) {
             int at = 0;
 #pragma unroll
-            for (int j = kUnroll - 1; j >= 0; --j) at = big[j] == all ? id + j * kThreads : at;
+            for (int j = kUnroll - 1; j >= 0; --j) at = big[j] == all ? id + j * T : at;
             // U is kept in units of log2 during the pass
             const float d = s.m > -INFINITY ? (s.m - all) * kLog2e : 0.0f, f = exp2_fast(d);
             s.u = f * fmaf(s.t, fmaxf(d, kFloor), s.u);
@@ -327,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a, int parts,
     if (k > 0) part_top(r, s, id0, id1, k, sh);
     else __syncthreads();
     Stat all = sh.stats[0];
-    for (int w = 1; w < kThreads / kWave; ++w) all = join(all, sh.stats[w]);
+    for (int w = 1; w < T / kWave; ++w) all = join(all, sh.stats[w]);
 
     if (parts == 1) {
         const float ref = all.m > -INFINITY ? all.m : 0.0f, log_t = logf(all.t);
@@ -342,7 +345,10 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a, int parts,
     // ---- leave the part's record, and join the row if it is the last one
     // Records are written and read as agent-scope words, which go past the
     // caches that other XCDs cannot see; a wave's stores are complete (vmcnt
-    // 0) before its barrier, so before the ticket is taken.
+    // 0) before its barrier, so before the ticket is taken.  The ticket itself
+    // needs no fences then: an acquire and release a workgroup writes back and
+    // empties its XCD's L2 each time (256 rows of
+    // 128256: 48 us with them, 31 without).
     const int words = score_record_words(k);
     uint32_t *rec = records + ((int64_t)row * parts + part) * words;
     if (tid == 0) {
@@ -363,8 +369,9 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a, int parts,
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (tid == 0) sh.last = tl::atomic_add_acqrel(tickets + row, 1) == parts - 1;
+    if (tid == 0) sh.last = tl::atomic_add_relaxed(tickets + row, 1) == parts - 1;
     __syncthreads();
+    asm volatile("" ::: "memory");
     if (!sh.last) return;
 
     const uint32_t *recs = records + (int64_t)row * parts * words;
@@ -391,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a, int parts,
     if (k == 0) return;
     // only the k lists whose first key reaches the k-th first key can matter
     const uint64_t bound = kth_of_64(sh.groups, k);
-    for (int i = tid; i < parts * k; i += kThreads) {
+    for (int i = tid; i < parts * k; i += T) {
         const int p = i / k, j = i % k;
         if (sh.groups[p] == 0 || sh.groups[p] < bound) continue;
         const uint32_t *q = recs + (int64_t)p * words + 4 + 2 * j;
@@ -409,9 +416,12 @@ __global__ __launch_bounds__(kThreads) void score_kernel(ScoreArgs a, int parts,
 hipError_t launch_token_logprobs(const ScoreArgs &a, const ScorePlan &plan, void *ws, hipStream_t st) {
     int32_t *tickets = static_cast<int32_t *>(ws);
     uint32_t *records = reinterpret_cast<uint32_t *>(static_cast<char *>(ws) + plan.ticket_bytes);
-    const dim3 grid((unsigned)a.n * plan.parts), block(kThreads);
-    if (a.fp32) score_kernel<true><<<grid, block, 0, st>>>(a, plan.parts, plan.part_ids, tickets, records);
-    else score_kernel<false><<<grid, block, 0, st>>>(a, plan.parts, plan.part_ids, tickets, records);
+    const dim3 grid((unsigned)a.n * plan.parts), block(plan.threads);
+    auto launch = [&](auto kernel) { kernel<<<grid, block, 0, st>>>(a, plan.parts, plan.part_ids, tickets, records); };
+    if (plan.threads == kScoreShortThreads)
+        launch(a.fp32 ? score_kernel<true, kScoreShortThreads> : score_kernel<false, kScoreShortThreads>);
+    else
+        launch(a.fp32 ? score_kernel<true, kScoreThreads> : score_kernel<false, kScoreThreads>);
     return hipGetLastError();
 }
 
