@@ -52,7 +52,7 @@ int step_rms_norm(const uint16_t *x, int64_t ldx, const uint16_t *residual, int6
 
 size_t step_lora_linear_workspace_bytes(int32_t n, int32_t k, int32_t out, int32_t num_slices, int32_t max_rank) {
     if (check_linear(n, k, out, num_slices, max_rank) != STEP_OK) return 0;
-    return st::linear_plan(n, num_slices, max_rank).total_bytes;
+    return st::linear_plan(n, out, num_slices, max_rank).total_bytes;
 }
 
 int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const uint8_t *xq, int64_t ldxq,
@@ -82,7 +82,7 @@ int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const
         return STEP_EINVAL;
     if (!aligned_or_null(xq, 16) || !aligned_or_null(x_scale, 4) || !aligned_or_null(w_scale, 4)) return STEP_EINVAL;
     if ((xq == nullptr) != (x_scale == nullptr) || (xq == nullptr) != (w_scale == nullptr)) return STEP_EINVAL;
-    const st::LinearPlan plan = st::linear_plan(n, num_slices, max_rank);
+    const st::LinearPlan plan = st::linear_plan(n, (int)out, num_slices, max_rank);
     if (!ws || ws_bytes < plan.total_bytes || !aligned(ws, 16)) return STEP_EWORKSPACE;
     a.x = x;
     a.ldx = ldx;

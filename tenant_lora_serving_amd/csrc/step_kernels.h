@@ -81,15 +81,15 @@ struct LinearArgs {
     uint16_t *y;
     int64_t ldy;
 };
-// Up to kUnsortedRows rows are taken as they come, more are sorted by slot
-// first.  The workspace holds the sorted rows' numbers and their slots
+// Up to kUnsortedRows rows are taken as they come (unless the product is
+// large), more are sorted by slot first.  The workspace holds the sorted rows' numbers and their slots
 // (row_words words each), then the inner sums.
 constexpr int kUnsortedRows = 256;
 struct LinearPlan {
     bool sorted;
     size_t row_words, total_bytes;
 };
-LinearPlan linear_plan(int n, int num_slices, int R);
+LinearPlan linear_plan(int n, int out, int num_slices, int R);
 struct LinearSpace {
     int32_t *perm, *key_of;
     uint16_t *xab;

@@ -440,10 +440,12 @@ double rounds_us(long long tiles, double fixed, double line, double lines) {
 template <Form F>
 void pick(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
     const int tiles = (out + 15) / 16;
-    if (a.n <= 16) return tiles > 768 ? go<F, 1, 2, 3>(a, h, out, st) : go<F, 1, 1, 4>(a, h, out, st);
+    // wide products from memory: tiles of 48 or 64 columns, of which two fit a CU
+    // (12 rows by 4096 x 32008: 60 us, in tiles of 32 columns 70)
+    if (a.n <= 16) return tiles > 768 ? go<F, 1, 4, 2>(a, h, out, st) : go<F, 1, 1, 4>(a, h, out, st);
     if (a.n <= 32) return tiles > 768 ? go<F, 2, 3, 2>(a, h, out, st) : go<F, 2, 1, 4>(a, h, out, st);
-    // (two workgroups a CU: 37 rows by 4096 x 32008 in 8 bits 45.7 us, 64 x 96 tiles 48.8)
-    if (a.n <= 48) return go<F, 3, 2, 2>(a, h, out, st);
+    // (37 rows by 4096 x 32008: 71.2 us, in 48 x 32 tiles 79.0, in 64 x 96 tiles 72.4)
+    if (a.n <= 48) return go<F, 3, 4, 2>(a, h, out, st);
     // the times below were fitted to single products (k 1008 to 4096)
     const double lines = (double)cdiv((long long)a.k * (F == kBf16 ? 2 : 1), kLine);
     auto small = [&](int nt) {

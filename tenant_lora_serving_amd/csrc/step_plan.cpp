@@ -42,9 +42,12 @@ ScorePlan score_plan(int n, int v, int top, int fp32) {
     return p;
 }
 
-LinearPlan linear_plan(int n, int num_slices, int R) {
+// Sorting costs a launch and some 5 us, and is needed for tiles larger than
+// 64 x 96: worth it past two rounds of those (a step with 256 rows by 4096 x 128256 took
+// 780 us without, 600 with).
+LinearPlan linear_plan(int n, int out, int num_slices, int R) {
     LinearPlan p{};
-    p.sorted = n > kUnsortedRows;
+    p.sorted = n > kUnsortedRows || (n > 64 && cdiv(n, 64) * cdiv(out, 96) > 512);
     const size_t inner = (size_t)n * num_slices * R * 2 * sizeof(uint16_t);
     if (p.sorted) p.row_words = up256((size_t)n * sizeof(int32_t)) / sizeof(int32_t);
     p.total_bytes = 2 * p.row_words * sizeof(int32_t) + up256(inner);

@@ -526,3 +526,12 @@ def test_linear_middling_broken_adapter(fp8):
     got = step.lora_linear(x, w, a, b, scale, widths, slot, **kw)
     assert not got[broken].isfinite().any()
     within(got[~broken], y[~broken], tol[~broken], "the others")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,k,widths,S,R", [(200, 272, (16392,), 50, 16), (100, 528, (20008, 6000), 9, 24),
+                                            (65, 80, (24584,), 65, 8), (256, 4096, (12296,), 4, 64)])
+def test_linear_few_rows_by_many_columns(n, k, widths, S, R, fp8):
+    print(f"linear wide n={n} k={k} widths={widths} S={S} R={R} fp8={fp8}", flush=True)
+    args, kw = linear_inputs(n + k, n, k, widths, S, R, fp8)
+    check_linear(args, kw, step.lora_linear(*args, **kw), "linear")
