@@ -156,19 +156,38 @@ __device__ __forceinline__ void apply_scales(const LinearArgs &a, float my_scale
 // Adds xab B_s^T for the slots of the rows in `mine` to a wave's tile of rows
 // from m0 (lane m holds row m's slot) and columns c0 .. c0 + cols: slice by
 // slice, in steps of 32 of the 2 R terms of one slot (R rounded inner sums and
-// R rests, against the same B twice), kSteps steps on the way.
+// R rests, against the same B twice), kSteps steps on the way.  With one wave a
+// SIMD its own instructions bound it: everything that a step does not change
+// is worked out before, and rows and columns that are not the step's read zero
+// through offsets past their buffers.
+// careful: a B is looked through for infinities and NaN, which are taken as
+// zero; true if there were any.
 constexpr int kSteps = 2;
+constexpr uint32_t kFar = 0x40000000u;  // past every buffer here, also with kOob added
 template <int MT, int NT>
-__device__ __forceinline__ void add_adapters(const LinearArgs &a, const uint16_t *xab, int out, int my_slot,
-                                             uint64_t mine, int m0, int c0, int cols, f32x4_t (&acc)[NT][MT],
-                                             int *any_broken) {
-    const int lane = tl::lane_id(), chunks = a.R / 8;
+__device__ __forceinline__ bool add_adapters(const LinearArgs &a, const uint16_t *xab, int out, int my_slot,
+                                             uint64_t mine, int m0, int rows, int c0, int cols, bool careful,
+                                             f32x4_t (&acc)[NT][MT]) {
+    if (!mine) return false;
+    bool broken = false;
+    const int lane = tl::lane_id(), chunks = a.R / 8, pitch = a.num_slices * 4 * a.R;
     int first_slice = 0, end_slice = a.num_slices;
     while (a.slice_off[first_slice + 1] <= c0) ++first_slice;
     while (end_slice > first_slice + 1 && a.slice_off[end_slice - 1] >= c0 + cols) --end_slice;
+    const rsrc_t xr = tl::make_rsrc(xab + (int64_t)m0 * a.num_slices * 2 * a.R, (uint32_t)(rows * pitch));
+    int row_slot[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) row_slot[i] = __shfl(my_slot, 16 * i + lane % 16);
+    const uint32_t x0 = (uint32_t)(lane % 16 * pitch);
 #pragma unroll 1
-    for (int slice = mine ? first_slice : end_slice; slice < end_slice; ++slice) {
+    for (int slice = first_slice; slice < end_slice; ++slice) {
         const int lo = a.slice_off[slice] - c0, hi = min(a.slice_off[slice + 1] - c0, cols);
+        uint32_t b0[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int c = 16 * j + lane % 16;
+            b0[j] = c >= lo && c < hi ? (uint32_t)(c * a.R * 2) : kFar;
+        }
         uint64_t todo = mine, same = 0;
         int slot = -1, q0 = 0;
         auto next_slot = [&]() {
@@ -183,21 +202,18 @@ __device__ __forceinline__ void add_adapters(const LinearArgs &a, const uint16_t
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 who[s] = same;
-                const int q = q0 + lane / 16, r = (q >= chunks ? q - chunks : q) * 8;
-                const bool in = q < 2 * chunks && slot >= 0;
-                const uint16_t *B = a.b_pool + ((int64_t)slot * out + c0) * a.R + r;
+                if (slot < 0) continue;
+                const int q = q0 + lane / 16;
+                const bool in = q < 2 * chunks;
+                const uint32_t bq = in ? (uint32_t)(q >= chunks ? q - chunks : q) * 16 : kOob;
+                const uint32_t xq = in ? (uint32_t)(slice * 4 * a.R + q * 16) : kOob;
+                const rsrc_t br = tl::make_rsrc(a.b_pool + ((int64_t)slot * out + c0) * a.R, (uint32_t)(cols * a.R * 2));
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int c = 16 * j + lane % 16;
-                    bf[s][j] = in && c >= lo && c < hi ? tl::ld16(B + (int64_t)c * a.R) : tl::zero4();
-                }
-                const uint16_t *X = xab + ((int64_t)m0 * a.num_slices + slice) * 2 * a.R + 8 * q;
+                for (int j = 0; j < NT; ++j) bf[s][j] = tl::buf_ld16(br, b0[j] + bq);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    const int m = 16 * i + lane % 16;
-                    xf[s][i] = in && (same >> m & 1) ? tl::ld16(X + (int64_t)m * a.num_slices * 2 * a.R) : tl::zero4();
-                }
-                if (slot >= 0 && (q0 += 4) >= 2 * chunks) next_slot();
+                for (int i = 0; i < MT; ++i)
+                    xf[s][i] = tl::buf_ld16(xr, row_slot[i] == slot ? x0 + xq + (uint32_t)(16 * i * pitch) : kOob);
+                if ((q0 += 4) >= 2 * chunks) next_slot();
             }
         };
         next_slot();
@@ -206,13 +222,16 @@ __device__ __forceinline__ void add_adapters(const LinearArgs &a, const uint16_t
         while (who[0]) {
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                u16x2_t big = {};
+                if (!who[s]) continue;
+                if (careful) {
+                    u16x2_t big = {};
 #pragma unroll
-                for (int j = 0; j < NT; ++j) big = larger_magnitude(big, bf[s][j]);
-                if (__ballot(not_finite(big))) {
-                    *any_broken = 1;
+                    for (int j = 0; j < NT; ++j) big = larger_magnitude(big, bf[s][j]);
+                    if (__ballot(not_finite(big))) {
+                        broken = true;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) drop_not_finite(bf[s][j]);
+                        for (int j = 0; j < NT; ++j) drop_not_finite(bf[s][j]);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -224,6 +243,19 @@ __device__ __forceinline__ void add_adapters(const LinearArgs &a, const uint16_t
             load_steps();
         }
     }
+    return broken;
+}
+// An infinity or NaN among a wave's results.
+template <int MT, int NT>
+__device__ __forceinline__ bool any_not_finite(const f32x4_t (&acc)[NT][MT]) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t = fmaf(acc[j][i][e], 0.0f, t);
+    return __ballot(t != t) != 0;
 }
 
 // SLOTS lines in a wave's ring.
@@ -261,24 +293,31 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, i
         const int m = Ring::row(u), r = SORTED ? __shfl(my_row, m) : m0 + m;
         xo[u] = m < rows ? (uint32_t)((int64_t)r * ldx) : kOob;
     }
-    f32x4_t acc[NT][MT] = {};
-    ring_product<F, NT, MT, SLOTS>(wr, wo, xr, xo, shared + wave * Ring::kBytes, wave, kWaves, lines, kbytes, acc);
-
-    if constexpr (FP8) apply_scales(a, lane < rows ? a.x_scale[my_row] : 0.0f, c0, cols, acc);
-
     // A wave takes the adapters whose slot is its number modulo kWaves: so a
     // row's sums meet in the same order whatever other rows share its tile, and
-    // the order of the sorted rows changes no result.
-    int *any_broken = reinterpret_cast<int *>(shared + kWaves * kShared) - 1;  // past what is written below
-    static_assert(kWaves * Part::kFloats * 4 <= kWaves * kShared - 4, "past the partial sums");
-    __syncthreads();
-    if (tid == 0) *any_broken = 0;
-    __syncthreads();
-    add_adapters<MT, NT>(a, h.xab, out, my_slot, __ballot(my_slot >= 0 && my_slot % kWaves == wave), m0, c0, cols, acc,
-                         any_broken);
+    // the order of the sorted rows changes no result.  Infinities and NaN are
+    // looked for in its sums, and only a wave that finds some computes them
+    // again with care (looking through every B cost 2 of 43 us).
+    const uint64_t mine = __ballot(my_slot >= 0 && my_slot % kWaves == wave);
+    f32x4_t acc[NT][MT];
+    bool careful = false, broken;
+#pragma unroll 1
+    for (;; careful = true) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[j][i] = f32x4_t{};
+        ring_product<F, NT, MT, SLOTS>(wr, wo, xr, xo, shared + wave * Ring::kBytes, wave, kWaves, lines, kbytes, acc);
+        if constexpr (FP8) apply_scales(a, lane < rows ? a.x_scale[my_row] : 0.0f, c0, cols, acc);
+        broken = add_adapters<MT, NT>(a, h.xab, out, my_slot, mine, m0, rows, c0, cols, careful, acc);
+        if (careful || !mine || !any_not_finite(acc)) break;
+    }
 
+    static_assert(kWaves * Part::kFloats * 4 <= kWaves * (kShared - 4), "the waves' words follow the partial sums");
+    int *broken_of = reinterpret_cast<int *>(shared + kWaves * kShared) - kWaves;
     __syncthreads();
     Part::put(red, wave, acc);
+    if (lane == 0) broken_of[wave] = broken;
     __syncthreads();
     for (int t = tid; t < Part::kRows * Part::kCols / 8; t += kThreads) {
         const int m = t / (Part::kCols / 8), c = t % (Part::kCols / 8) * 8;
@@ -288,7 +327,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, i
         const int64_t r = SORTED ? h.perm[m0 + m] : m0 + m;
         tl::st16(a.y + r * a.ldy + c0 + c, pack8(v));
     }
-    if (*any_broken)
+    if (broken_of[0] | broken_of[1] | broken_of[2] | broken_of[3])
         mark_broken<kThreads>(a, out, m0, rows, c0, cols, SORTED ? h.perm : nullptr, SORTED ? h.key_of : a.slot);
 }
 
@@ -304,8 +343,7 @@ constexpr int kMidTile = 128, kMidSlots = 4, kMidLoads = 8, kMidSlot = 2 * kMidT
 template <Form F>
 __global__ __launch_bounds__(kThreads) void mid_kernel(LinearArgs a, Inner h, int out) {
     __shared__ __align__(16) char lds[kMidSlots * kMidSlot];
-    const int lane = tl::lane_id(), tid = threadIdx.x;
-    const int wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
+    const int lane = tl::lane_id(), wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
     // row tiles of the same columns run next to each other on one XCD
     const int m_tiles = (a.n + kMidTile - 1) / kMidTile, on_xcd = blockIdx.x / 8;
     const int c0 = (on_xcd / m_tiles * 8 + blockIdx.x % 8) * kMidTile, m0 = on_xcd % m_tiles * kMidTile;
@@ -378,10 +416,7 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(LinearArgs a, Inner h, in
         }
     }
     wait_loads<0>();  // (lines past the end still write zeros)
-    int &any_broken = *reinterpret_cast<int *>(lds);
-    __syncthreads();
-    if (tid == 0) any_broken = 0;
-    __syncthreads();
+    bool broken = false;
 
     // ---- this wave's 64 x 64
     const int m1 = m0 + wm, c1 = c0 + wn, my_rows = rows - wm, my_cols = min(cols - wn, 64);
@@ -390,7 +425,7 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(LinearArgs a, Inner h, in
     const int my_slot = key < a.num_slots ? key : -1;
     if (my_rows > 0 && my_cols > 0) {
         if constexpr (F != kBf16) apply_scales(a, here ? a.x_scale[my_row] : 0.0f, c1, my_cols, acc);
-        add_adapters<4, 4>(a, h.xab, out, my_slot, __ballot(my_slot >= 0), m1, c1, my_cols, acc, &any_broken);
+        broken = add_adapters<4, 4>(a, h.xab, out, my_slot, __ballot(my_slot >= 0), m1, my_rows, c1, my_cols, true, acc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int m = 16 * i + lane % 16, r = __shfl(my_row, m);
@@ -405,9 +440,11 @@ __global__ __launch_bounds__(kThreads) void mid_kernel(LinearArgs a, Inner h, in
             }
         }
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // before another thread may write a result again
+    int *broken_of = reinterpret_cast<int *>(lds);  // (every wave is past its reads of lines)
     __syncthreads();
-    if (any_broken) mark_broken<kThreads>(a, out, m0, rows, c0, cols, h.perm, h.key_of);
+    if (lane == 0) broken_of[wave] = broken;
+    __syncthreads();
+    if (broken_of[0] | broken_of[1] | broken_of[2] | broken_of[3]) mark_broken<kThreads>(a, out, m0, rows, c0, cols, h.perm, h.key_of);
 }
 
 template <Form F, int MT, int NT, int SLOTS>
