@@ -18,7 +18,8 @@
 // workgroup.  The waves of a workgroup share one tile and take every
 // kWaves-th line of k through rings of their own, so nothing that a wave
 // loads is another's too and there is no barrier in the loop.  The waves'
-// sums meet in shared memory once, at the end.
+// sums meet in shared memory once, at the end.  One row by 4096 x 6144: 11 us of
+// 18, 4.6 TB/s; 256 rows: 27 of 39 us.
 #include "step_linear.h"
 
 namespace st {
@@ -337,8 +338,9 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, i
 // often.  Lines go through kMidSlots buffers of LDS that the waves share; a
 // wave multiplies a line from registers while it reads the next one's
 // fragments, two matrix instructions to a read, and the loads of two more
-// lines are out: a line keeps the matrix cores and the LDS busy for 512 and
-// 768 cycles.
+// lines are out.  A line keeps the matrix cores and the LDS busy for 512 and
+// 768 cycles and takes some 1300 (1000 rows by 4096 x 6144: 80 us, in 64 x 64
+// tiles 100; in 256 x 256 tiles they would be a third of the chip).
 constexpr int kMidTile = 128, kMidSlots = 4, kMidLoads = 8, kMidSlot = 2 * kMidTile * kLine;
 template <Form F>
 __global__ __launch_bounds__(kThreads) void mid_kernel(LinearArgs a, Inner h, int out) {

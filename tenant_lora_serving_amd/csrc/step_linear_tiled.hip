@@ -18,6 +18,8 @@
 // wave multiplies while the other reads.  A part of a buffer is refilled two
 // phases after its last read and used six phases after its refill was
 // started, so the wait is for loads that are 5 phases (10 loads) old.
+// 6947 rows by 4096 x 28672 with rank-64 adapters: 1.2 PFLOP/s in bf16, 2.0 to
+// 2.1 in e4m3, with the matrix cores busy 60% of the cycles in bf16.
 #include "step_linear.h"
 
 namespace st {

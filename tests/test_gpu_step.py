@@ -535,3 +535,10 @@ def test_linear_few_rows_by_many_columns(n, k, widths, S, R, fp8):
     print(f"linear wide n={n} k={k} widths={widths} S={S} R={R} fp8={fp8}", flush=True)
     args, kw = linear_inputs(n + k, n, k, widths, S, R, fp8)
     check_linear(args, kw, step.lora_linear(*args, **kw), "linear")
+
+
+def test_norm_of_more_rows_than_one_side_of_a_grid():
+    n, h = (1 << 22) + 5, 8         # four rows a workgroup, 2^20 workgroups a side
+    x = randn(gen(6), n, h).bfloat16()
+    w = (1 + randn(gen(7), h, std=0.1)).bfloat16()
+    check_norm(x, None, w, True, True, step.rms_norm(x, w, EPS, quant=True))
