@@ -29,59 +29,75 @@ namespace {
 // ---------------------------------------------------------------- inner sums
 constexpr int kInWaves = 8, kInThreads = kInWaves * kWave;
 
-// The t-th group of up to 16 rows of one slot, numbered slot by slot; count 0
-// past the last group.  Lane m < count holds row m's number.  Every wave finds
-// it by itself, from ballots: ranks through LDS, with their barriers, took
-// 4 us more for some hundred rows.
+// The t-th group of up to 16 rows of one slot, numbered by the row that it
+// starts with; count 0 past the last group.  Lane m < count holds row m's
+// number.  Every wave finds it by itself: the lanes with a row's slot follow
+// from one ballot a bit of the slot's number, so the time grows with
+// log(slots).  (Slot after slot took 12 us of the kernel for 256 rows over 32
+// slots and 46 over 128, ranks through LDS some 4 for their barriers.)
 struct Group {
     int slot, count, row;
 };
+// kChunks: of 64 rows, all rows.
+template <int kChunks>
 __device__ __forceinline__ Group find_group(const LinearArgs &a, int t) {
-    constexpr int kChunks = kUnsortedRows / kWave;
-    const int lane = tl::lane_id();
-    int s[kChunks], before = 0;
-    uint64_t todo[kChunks], same[kChunks];
+    const int lane = tl::lane_id(), chunks = (a.n + kWave - 1) / kWave;
+    const int bits = a.num_slots > 1 ? 32 - __builtin_clz(a.num_slots - 1) : 0;
+    int s[kChunks];
+    uint64_t same[kChunks][kChunks];  // [c][d]: the rows of chunk d with the slot of the lane's row in chunk c
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
         s[c] = c * kWave + lane < a.n ? a.slot[c * kWave + lane] : -1;
-        todo[c] = __ballot(s[c] >= 0 && s[c] < a.num_slots);
+        if (s[c] >= a.num_slots) s[c] = -1;
     }
-    for (;;) {
-        int slot = -1;
 #pragma unroll
-        for (int c = kChunks - 1; c >= 0; --c)
-            if (todo[c]) slot = __builtin_amdgcn_readlane(s[c], __builtin_ctzll(todo[c]));
-        if (slot < 0) return {-1, 0, 0};
-        int rows = 0;
+    for (int d = 0; d < kChunks; ++d) {
+        const uint64_t valid = __ballot(s[d] >= 0);
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            same[c] = __ballot(s[c] == slot);
-            todo[c] &= ~same[c];
-            rows += __popcll(same[c]);
-        }
-        const int groups = (rows + 15) / 16;
-        if (t >= before + groups) {
-            before += groups;
-            continue;
-        }
-        // each of the group's lanes hands its row's number + 1 to the lane of
-        // its place in the group, the others a 0 to the last lane
-        const int first = (t - before) * 16;
-        int at = -first, row = 0;
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int i = at + __popcll(same[c] & tl::lanemask_lt());
-            const bool mine = (same[c] >> lane & 1) && i >= 0 && i < 16;
-            row = max(row, __builtin_amdgcn_ds_permute((mine ? i : kWave - 1) * 4, mine ? c * kWave + lane + 1 : 0));
-            at += __popcll(same[c]);
-        }
-        return {slot, min(rows - first, 16), row - 1};
+        for (int c = d; c < kChunks; ++c) same[c][d] = valid;
     }
+#pragma unroll 1
+    for (int b = 0; b < bits; ++b) {
+#pragma unroll
+        for (int d = 0; d < kChunks; ++d) {
+            if (d > 0 && d >= chunks) break;
+            const uint64_t set = __ballot(s[d] >> b & 1);
+#pragma unroll
+            for (int c = d; c < kChunks; ++c) same[c][d] &= s[c] >> b & 1 ? set : ~set;
+        }
+    }
+    // ranks among the slot's rows; every 16th leads a group
+    int rank[kChunks], before = 0, slot = -1, first = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        rank[c] = __popcll(same[c][c] & tl::lanemask_lt());
+#pragma unroll
+        for (int d = 0; d < c; ++d) rank[c] += __popcll(same[c][d]);
+        const uint64_t leads = __ballot(s[c] >= 0 && rank[c] % 16 == 0);
+        const uint64_t it = __ballot((leads >> lane & 1) && before + __popcll(leads & tl::lanemask_lt()) == t);
+        if (it) {
+            slot = __builtin_amdgcn_readlane(s[c], __builtin_ctzll(it));
+            first = __builtin_amdgcn_readlane(rank[c], __builtin_ctzll(it));
+        }
+        before += __popcll(leads);
+    }
+    if (slot < 0) return {-1, 0, 0};
+    // each of the group's lanes hands its row's number + 1 to the lane of its
+    // place in the group, the others a 0 to the last lane
+    int row = 0, count = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int i = rank[c] - first;
+        const bool mine = s[c] == slot && i >= 0 && i < 16;
+        row = max(row, __builtin_amdgcn_ds_permute((mine ? i : kWave - 1) * 4, mine ? c * kWave + lane + 1 : 0));
+        count += __popcll(__ballot(mine));
+    }
+    return {slot, count, row - 1};
 }
 
 // A group of rows by 16 NT of the num_slices * R rows of A_s.  Eight waves
 // split k, so that each has only a few lines to wait for.
-template <int NT, int SLOTS>
+template <int NT, int SLOTS, int CHUNKS>
 __global__ __launch_bounds__(kInThreads) void inner_kernel(LinearArgs a, uint16_t *xab) {
     using Part = Partials<NT, 1>;
     using Ring = LineRing<NT, 1, SLOTS>;
@@ -91,7 +107,7 @@ __global__ __launch_bounds__(kInThreads) void inner_kernel(LinearArgs a, uint16_
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tl::wave_id());
     const int LR = a.num_slices * a.R, kbytes = a.k * 2, lines = (kbytes + kLine - 1) / kLine;
     const int c0 = blockIdx.y * Part::kCols;
-    const Group group = find_group(a, blockIdx.x);
+    const Group group = find_group<CHUNKS>(a, blockIdx.x);
     const int slot = __builtin_amdgcn_readfirstlane(group.slot), count = __builtin_amdgcn_readfirstlane(group.count);
     const int row = group.row;
     if (count == 0) return;
@@ -514,11 +530,12 @@ hipError_t launch_lora_linear(const LinearArgs &a, const LinearPlan &plan, void 
     } else {
         // groups of up to 16 rows of one slot: every slot ends one that is not full
         const int most = a.n / 16 + a.num_slots, groups = a.n < most ? a.n : most, LR = a.num_slices * a.R;
+        const dim3 narrow(groups, (LR + 15) / 16), wide(groups, (LR + 63) / 64);
+        constexpr int kAll = kUnsortedRows / kWave;
         // (1168 units of 16 columns took 83 us where 236 of 64 take 50)
-        if (groups * ((LR + 15) / 16) <= 512)
-            inner_kernel<1, 4><<<dim3(groups, (LR + 15) / 16), kInThreads, 0, st>>>(a, s.xab);
-        else
-            inner_kernel<4, 2><<<dim3(groups, (LR + 63) / 64), kInThreads, 0, st>>>(a, s.xab);
+        if (narrow.x * narrow.y > 512) inner_kernel<4, 2, kAll><<<wide, kInThreads, 0, st>>>(a, s.xab);
+        else if (a.n > kWave) inner_kernel<1, 4, kAll><<<narrow, kInThreads, 0, st>>>(a, s.xab);
+        else inner_kernel<1, 4, 1><<<narrow, kInThreads, 0, st>>>(a, s.xab);
     }
     const Inner h{plan.sorted ? s.perm : nullptr, s.key_of, s.xab};
     if (a.xq && a.k <= kExactK) pick<kE4m3AsBf16>(a, h, out, st);
