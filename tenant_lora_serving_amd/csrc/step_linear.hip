@@ -18,8 +18,8 @@
 // workgroup.  The waves of a workgroup share one tile and take every
 // kWaves-th line of k through rings of their own, so nothing that a wave
 // loads is another's too and there is no barrier in the loop.  The waves'
-// sums meet in shared memory once, at the end.  One row by 4096 x 6144: 11 us of
-// 18, 4.6 TB/s; 256 rows: 27 of 39 us.
+// sums meet in shared memory once, at the end.  One row by 4096 x 6144: 10 us of
+// 17, 5 TB/s; 256 rows: 27 of 35 us.
 #include "step_linear.h"
 
 namespace st {
@@ -316,6 +316,8 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, i
     // looked for in its sums, and only a wave that finds some computes them
     // again with care (looking through every B cost 2 of 43 us).
     const uint64_t mine = __ballot(my_slot >= 0 && my_slot % kWaves == wave);
+    // (not where row tiles share x: 139 rows by 11312 x 9656 took 141 us so, 134 in step)
+    const int turn = m_tiles == 1 ? c0 / Part::kCols * 7 % lines : 0;
     f32x4_t acc[NT][MT];
     bool careful = false, broken;
 #pragma unroll 1
@@ -324,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(LinearArgs a, Inner h, i
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int i = 0; i < MT; ++i) acc[j][i] = f32x4_t{};
-        ring_product<F, NT, MT, SLOTS>(wr, wo, xr, xo, shared + wave * Ring::kBytes, wave, kWaves, lines, kbytes, acc);
+        ring_product<F, NT, MT, SLOTS>(wr, wo, xr, xo, shared + wave * Ring::kBytes, wave, kWaves, lines, kbytes, acc, turn);
         if constexpr (FP8) apply_scales(a, lane < rows ? a.x_scale[my_row] : 0.0f, c0, cols, acc);
         broken = add_adapters<MT, NT>(a, h.xab, out, my_slot, mine, m0, rows, c0, cols, careful, acc);
         if (careful || !mine || !any_not_finite(acc)) break;
