@@ -64,7 +64,8 @@ int step_rms_norm(const uint16_t *x, int64_t ldx, const uint16_t *residual, int6
                   void *stream);
 
 /* Workspace bytes step_lora_linear needs: `out` is the sum of the slice
- * widths.  0 for a shape that the call refuses. */
+ * widths.  0 for a shape that the call refuses.  They serve every call of the
+ * same or smaller sizes too. */
 size_t step_lora_linear_workspace_bytes(int32_t n, int32_t k, int32_t out, int32_t num_slices, int32_t max_rank);
 
 /*
@@ -102,7 +103,8 @@ int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const
                      const int32_t *slice_sizes, int32_t max_rank, const int32_t *slot, uint16_t *y, int64_t ldy,
                      void *ws, size_t ws_bytes, void *stream);
 
-/* Workspace bytes step_token_logprobs needs (0 for a shape that it refuses). */
+/* Workspace bytes step_token_logprobs needs (0 for a shape that it refuses).
+ * They serve every call of the same or smaller n, v and top too. */
 size_t step_token_logprobs_workspace_bytes(int32_t n, int32_t v, int32_t top);
 
 /*

@@ -107,8 +107,7 @@ int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const
 
 size_t step_token_logprobs_workspace_bytes(int32_t n, int32_t v, int32_t top) {
     if (check_score(n, v, top) != STEP_OK) return 0;
-    const size_t a = st::score_plan(n, v, top, 0).total_bytes, b = st::score_plan(n, v, top, 1).total_bytes;
-    return a > b ? a : b;
+    return n > 0 ? st::score_workspace_bytes(n, v, top) : 0;
 }
 
 int step_token_logprobs(const void *logits, int64_t ld, int32_t fp32, int32_t n, int32_t v, const int32_t *tokens,

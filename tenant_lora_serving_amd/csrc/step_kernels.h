@@ -37,6 +37,7 @@ constexpr int kScoreMaxParts = 64;
 // The tickets (a word a row, 0 between calls) have a place of their own, the
 // same for every shape, so that no call's records are another's tickets.
 constexpr int kScoreMaxRows = 1 << 16;
+constexpr size_t kScoreTicketBytes = (size_t)kScoreMaxRows * sizeof(int32_t);
 // What a piece leaves in the workspace, in 32-bit words: maximum, two sums, a
 // count, then `top` 64-bit keys as (high, low).
 __host__ __device__ inline int score_record_words(int top) { return 4 + 2 * top; }
@@ -46,6 +47,9 @@ struct ScorePlan {
     size_t ticket_bytes, total_bytes;
 };
 ScorePlan score_plan(int n, int v, int top, int fp32);
+// Enough for every plan of at most n rows, v logits a row and `top`
+// alternatives, of both types.
+size_t score_workspace_bytes(int n, int v, int top);
 struct ScoreArgs {
     const void *logits;
     int64_t ld;

@@ -9,14 +9,26 @@ namespace {
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
+// A row of logits as 16-byte vectors: whole ones and the two ragged ends.
+long long score_ids(int v, int fp32) { return v / (fp32 ? 4 : 8) + 2; }
+// The fewest pieces of a row: as many as keep a thread within kScoreLaneElems
+// logits; and the most: as many as leave each thread one vector.
+long long score_least(long long ids, int fp32) {
+    return cdiv(ids, (long long)kScoreThreads * (kScoreLaneElems / (fp32 ? 4 : 8)));
+}
+long long score_most(long long ids) {
+    const long long m = cdiv(ids, kScoreThreads);
+    return m < kScoreMaxParts ? m : kScoreMaxParts;
+}
+// Pieces of all rows together that few rows are cut into, about two per CU.
+constexpr int kScorePieces = 512;
+
 }  // namespace
 
-// At least as many pieces as keep a thread within kScoreLaneElems logits; for
-// few rows more, until the pieces number about two per CU, but not so many
-// that a thread has less than one 16-byte vector.
+// The fewest pieces for many rows; for few rows more, until the pieces number
+// about two per CU, but not so many that a thread has less than one vector.
 ScorePlan score_plan(int n, int v, int top, int fp32) {
-    const int E = fp32 ? 4 : 8;
-    const long long ids = v / E + 2;  // whole vectors and the two ragged ends
+    const long long ids = score_ids(v, fp32);
     ScorePlan p{};
     // enough rows to fill the chip, and each within eight vectors of 128
     // threads: 2000 rows of 1417 floats, top 1: 10 us; with 512
@@ -28,18 +40,37 @@ ScorePlan score_plan(int n, int v, int top, int fp32) {
         return p;
     }
     p.threads = kScoreThreads;
-    const long long least = cdiv(ids, (long long)kScoreThreads * (kScoreLaneElems / E));
-    long long parts = cdiv(512, n > 0 ? n : 1);
-    if (parts > cdiv(ids, kScoreThreads)) parts = cdiv(ids, kScoreThreads);
-    if (parts > kScoreMaxParts) parts = kScoreMaxParts;
+    const long long least = score_least(ids, fp32), most = score_most(ids);
+    long long parts = cdiv(kScorePieces, n > 0 ? n : 1);
+    if (parts > most) parts = most;
     if (parts < least) parts = least;
     p.part_ids = (int)cdiv(ids, parts);
     p.parts = (int)cdiv(ids, p.part_ids);
     if (p.parts > 1) {
-        p.ticket_bytes = (size_t)kScoreMaxRows * sizeof(int32_t);
+        p.ticket_bytes = kScoreTicketBytes;
         p.total_bytes = p.ticket_bytes + up256((size_t)n * p.parts * score_record_words(top) * sizeof(uint32_t));
     }
     return p;
+}
+
+// Fewer rows are cut into more pieces, so what n rows need does not bound what
+// fewer need.  For m <= n rows a plan has at most m * least or, where that
+// leaves room for more, m * min(most, cdiv(kScorePieces, m)) pieces, which is
+// at most kScorePieces - 1 + m and, past kScorePieces rows, one a row, which
+// leaves no record.
+size_t score_workspace_bytes(int n, int v, int top) {
+    long long pieces = 0;
+    for (int fp32 = 0; fp32 < 2; ++fp32) {
+        const long long ids = score_ids(v, fp32), least = score_least(ids, fp32), most = score_most(ids);
+        const long long few = n < kScorePieces ? n : kScorePieces - 1;
+        long long p = least > 1 ? n * least : 0;
+        if (most > 1) {
+            const long long spread = few * most < kScorePieces - 1 + few ? few * most : kScorePieces - 1 + few;
+            if (spread > p) p = spread;
+        }
+        if (p > pieces) pieces = p;
+    }
+    return pieces ? kScoreTicketBytes + up256((size_t)pieces * score_record_words(top) * sizeof(uint32_t)) : 0;
 }
 
 // Sorting costs a launch and some 5 us, and is needed for tiles larger than

@@ -155,6 +155,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, *, residu
 
 # ---------------------------------------------------------------- projection
 def linear_workspace(n: int, k: int, out: int, num_slices: int, max_rank: int, device="cuda") -> torch.Tensor:
+    """A workspace for calls of at most these sizes."""
     b = int(lib().step_lora_linear_workspace_bytes(n, k, out, num_slices, max_rank))
     return torch.zeros(max(b, 16), dtype=torch.uint8, device=device)
 
@@ -229,6 +230,7 @@ class LogprobResult(NamedTuple):
 
 
 def logprobs_workspace(n: int, v: int, top: int = 0, device="cuda") -> torch.Tensor:
+    """A workspace for calls of at most n rows, v logits a row and `top` alternatives."""
     b = int(lib().step_token_logprobs_workspace_bytes(n, v, top))
     return torch.zeros(max(b, 16), dtype=torch.uint8, device=device)
 

@@ -1,0 +1,84 @@
+"""What step.h's entry points accept, refuse and plan, on a host-only build of
+them (step_abi.cpp and step_plan.cpp with the launchers replaced by the stubs
+in step_host_stubs.cpp), so that accepted calls can be tested without a GPU."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "tenant_lora_serving_amd", "csrc")
+OK, EINVAL, EUNSUP, EWS = 0, -1, -2, -3
+NORM, LINEAR, SCORE = range(3)
+
+
+@pytest.fixture(scope="module")
+def L(tmp_path_factory):
+    if not shutil.which("g++"):
+        pytest.skip("g++ is not available")
+    path = str(tmp_path_factory.mktemp("step") / "libstep_host.so")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__",
+                    "-I", "/opt/rocm/include", "-I", os.path.join(ROOT, "include"),
+                    os.path.join(CSRC, "step_abi.cpp"), os.path.join(CSRC, "step_plan.cpp"),
+                    os.path.join(ROOT, "tests", "step_host_stubs.cpp"), "-o", path], check=True)
+    L = ctypes.CDLL(path)
+    i32, i64, p, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+    L.step_lora_linear.argtypes = [p, i64, i32, i32, p, i64, p, p, p, p, p, p, i32, i32, p, i32, p, p, i64, p, sz, p]
+    L.step_token_logprobs.argtypes = [p, i64, i32, i32, i32, p, i32, p, p, p, p, p, p, sz, p]
+    L.step_lora_linear_workspace_bytes.restype = L.step_token_logprobs_workspace_bytes.restype = sz
+    L.step_lora_linear_workspace_bytes.argtypes = [i32] * 5
+    L.step_token_logprobs_workspace_bytes.argtypes = [i32] * 3
+    L.stub_calls.restype = ctypes.c_longlong
+    return L
+
+
+@pytest.fixture(autouse=True)
+def reset(L):
+    L.stub_reset()
+
+
+def score(L, n, v, top, ws_bytes, fp32=0):
+    tops = (0x6000, 0x7000) if top else (None, None)
+    return L.step_token_logprobs(0x1000, v, fp32, n, v, 0x2000, top, 0x3000, 0x4000, 0x5000, *tops, 0x8000, ws_bytes,
+                                 None)
+
+
+VOCABS = [1, 4096, 4097, 8180, 8190, 32000, 32750, 32760, 32770, 65500, 128256, 262143, 262144, 524288, 1 << 20]
+
+
+@pytest.mark.parametrize("v", VOCABS)
+def test_score_workspace_serves_every_smaller_batch(L, v):
+    """A workspace sized for n rows is accepted for any fewer rows, whatever the type."""
+    size, top = L.step_token_logprobs_workspace_bytes, 5
+    rows = [*range(1, 140), 170, 171, 255, 256, 257, 300, 511, 512, 513, 700, 1 << 16]
+    sizes = [size(n, v, top) for n in rows]
+    assert sizes == sorted(sizes)
+    for most, have in zip(rows, sizes):
+        for n in rows:
+            if n > most:
+                break
+            for fp32 in (0, 1):
+                assert score(L, n, v, top, have, fp32) == OK, (most, n, fp32)
+
+
+def test_score_workspace_grows_with_every_size(L):
+    size = L.step_token_logprobs_workspace_bytes
+    for n in (1, 100, 512, 3000):
+        for top in (0, 5, 32):
+            by_v = [size(n, v, top) for v in VOCABS]
+            assert by_v == sorted(by_v)
+        for v in VOCABS:
+            by_top = [size(n, v, top) for top in range(33)]
+            assert by_top == sorted(by_top)
+
+
+def test_linear_workspace_grows_with_every_size(L):
+    size = L.step_lora_linear_workspace_bytes
+    for out in (8, 96, 6144, 8192, 32008, 1 << 20):
+        by_n = [size(n, 4096, out, 3, 16) for n in range(1, 400)]
+        assert by_n == sorted(by_n)
+    for n in (1, 64, 65, 128, 256, 257):
+        by_out = [size(n, 4096, out, 3, 16) for out in range(8, 40000, 8)]
+        assert by_out == sorted(by_out)
