@@ -94,6 +94,10 @@ struct LinearPlan {
     size_t row_words, total_bytes;
 };
 LinearPlan linear_plan(int n, int out, int num_slices, int R);
+// Rows x columns of the tiles that the product is computed in; the last two
+// need sorted rows.
+enum Tile { k16x16, k16x64, k32x16, k32x48, k48x64, k64x32, k64x64, k64x96, k128x128, k256x256 };
+Tile linear_tile(int n, int k, int out, bool fp8, bool sorted);
 struct LinearSpace {
     int32_t *perm, *key_of;
     uint16_t *xab;

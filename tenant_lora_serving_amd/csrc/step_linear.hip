@@ -486,39 +486,23 @@ void go_mid(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
     mid_kernel<F><<<dim3((unsigned)((c_tiles + 7) / 8 * 8) * m_tiles), kThreads, 0, st>>>(a, h, out);
 }
 
-long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
-
-// Microseconds of a product of `tiles` tiles, one a CU at a time: `fixed` and
-// `line` those of a tile and of a line of its k.
-double rounds_us(long long tiles, double fixed, double line, double lines) {
-    return 8.0 + (double)cdiv(tiles, 256) * (fixed + line * lines);
-}
-
 template <Form F>
-void pick(const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
-    const int tiles = (out + 15) / 16;
-    // wide products from memory: tiles of 48 or 64 columns, of which two fit a CU
-    // (12 rows by 4096 x 32008: 60 us, in tiles of 32 columns 70)
-    if (a.n <= 16) return tiles > 768 ? go<F, 1, 4, 2>(a, h, out, st) : go<F, 1, 1, 4>(a, h, out, st);
-    if (a.n <= 32) return tiles > 768 ? go<F, 2, 3, 2>(a, h, out, st) : go<F, 2, 1, 4>(a, h, out, st);
-    // (37 rows by 4096 x 32008: 71.2 us, in 48 x 32 tiles 79.0, in 64 x 96 tiles 72.4)
-    if (a.n <= 48) return go<F, 3, 4, 2>(a, h, out, st);
-    // the times below were fitted to single products (k 1008 to 4096)
-    const double lines = (double)cdiv((long long)a.k * (F == kBf16 ? 2 : 1), kLine);
-    auto small = [&](int nt) {
-        return rounds_us(cdiv(tiles, nt) * cdiv(a.n, 64), 4.0, 0.11 * (4 + nt), (double)cdiv((long long)lines, kWaves));
-    };
-    const double s2 = small(2), s4 = small(4), s6 = small(6), best = s2 < s4 ? (s2 < s6 ? s2 : s6) : (s4 < s6 ? s4 : s6);
-    if constexpr (F != kE4m3AsBf16) {
-        if (h.perm) {
-            const double mid = rounds_us(cdiv(out, kMidTile) * cdiv(a.n, kMidTile), 4.0, 0.58, lines);
-            const double large = rounds_us(cdiv(out, 256) * cdiv(a.n, 256), 8.0, F == kBf16 ? 1.6 : 1.8, lines);
-            if (large <= mid && large <= best) return launch_lora_linear_tiled(a, h.perm, h.key_of, h.xab, st);
-            if (mid <= best) return go_mid<F>(a, h, out, st);
-        }
+void multiply(Tile tile, const LinearArgs &a, const Inner &h, int out, hipStream_t st) {
+    switch (tile) {
+        case k16x16: return go<F, 1, 1, 4>(a, h, out, st);
+        case k16x64: return go<F, 1, 4, 2>(a, h, out, st);
+        case k32x16: return go<F, 2, 1, 4>(a, h, out, st);
+        case k32x48: return go<F, 2, 3, 2>(a, h, out, st);
+        case k48x64: return go<F, 3, 4, 2>(a, h, out, st);
+        case k64x32: return go<F, 4, 2, 3>(a, h, out, st);
+        case k64x64: return go<F, 4, 4, 2>(a, h, out, st);
+        case k64x96: return go<F, 4, 6, 2>(a, h, out, st);
+        default: break;
     }
-    if (s6 <= best) return go<F, 4, 6, 2>(a, h, out, st);
-    return s4 <= best ? go<F, 4, 4, 2>(a, h, out, st) : go<F, 4, 2, 3>(a, h, out, st);
+    if constexpr (F != kE4m3AsBf16) {
+        if (tile == k128x128) go_mid<F>(a, h, out, st);
+        else launch_lora_linear_tiled(a, h.perm, h.key_of, h.xab, st);
+    }
 }
 
 }  // namespace
@@ -540,9 +524,10 @@ hipError_t launch_lora_linear(const LinearArgs &a, const LinearPlan &plan, void 
         else inner_kernel<1, 4, 1><<<narrow, kInThreads, 0, st>>>(a, s.xab);
     }
     const Inner h{plan.sorted ? s.perm : nullptr, s.key_of, s.xab};
-    if (a.xq && a.k <= kExactK) pick<kE4m3AsBf16>(a, h, out, st);
-    else if (a.xq) pick<kE4m3>(a, h, out, st);
-    else pick<kBf16>(a, h, out, st);
+    const Tile tile = linear_tile(a.n, a.k, out, a.xq != nullptr, plan.sorted);
+    if (a.xq && a.k <= kExactK) multiply<kE4m3AsBf16>(tile, a, h, out, st);
+    else if (a.xq) multiply<kE4m3>(tile, a, h, out, st);
+    else multiply<kBf16>(tile, a, h, out, st);
     return hipGetLastError();
 }
 

@@ -1,5 +1,5 @@
-// step_plan.cpp -- host-side sizing of step.h's calls: how a row of logits and
-// the inner sums of a projection are cut, and what their workspaces hold.
+// step_plan.cpp -- host-side sizing of step.h's calls: how a row of logits, a
+// projection and its inner sums are cut, and what their workspaces hold.
 #include "step_kernels.h"
 
 namespace st {
@@ -83,6 +83,36 @@ LinearPlan linear_plan(int n, int out, int num_slices, int R) {
     if (p.sorted) p.row_words = up256((size_t)n * sizeof(int32_t)) / sizeof(int32_t);
     p.total_bytes = 2 * p.row_words * sizeof(int32_t) + up256(inner);
     return p;
+}
+
+// Microseconds of a product of `tiles` tiles, one a CU at a time: `fixed` and
+// `line` those of a tile and of a line of its k.
+static double rounds_us(long long tiles, double fixed, double line, double lines) {
+    return 8.0 + (double)cdiv(tiles, 256) * (fixed + line * lines);
+}
+
+Tile linear_tile(int n, int k, int out, bool fp8, bool sorted) {
+    const int tiles = (out + 15) / 16;
+    // wide products from memory: tiles of 48 or 64 columns, of which two fit a CU
+    // (12 rows by 4096 x 32008: 60 us, in tiles of 32 columns 70)
+    if (n <= 16) return tiles > 768 ? k16x64 : k16x16;
+    if (n <= 32) return tiles > 768 ? k32x48 : k32x16;
+    // (37 rows by 4096 x 32008: 71.2 us, in 48 x 32 tiles 79.0, in 64 x 96 tiles 72.4)
+    if (n <= 48) return k48x64;
+    // the times below were fitted to single products (k 1008 to 4096)
+    const double lines = (double)cdiv((long long)k * (fp8 ? 1 : 2), 128);  // of 128 bytes
+    auto small = [&](int nt) {
+        return rounds_us(cdiv(tiles, nt) * cdiv(n, 64), 4.0, 0.11 * (4 + nt), (double)cdiv((long long)lines, 4));  // four waves share the lines
+    };
+    const double s2 = small(2), s4 = small(4), s6 = small(6), best = s2 < s4 ? (s2 < s6 ? s2 : s6) : (s4 < s6 ? s4 : s6);
+    if (sorted && !(fp8 && k <= kExactK)) {
+        const double mid = rounds_us(cdiv(out, 128) * cdiv(n, 128), 4.0, 0.58, lines);
+        const double large = rounds_us(cdiv(out, 256) * cdiv(n, 256), 8.0, fp8 ? 1.8 : 1.6, lines);
+        if (large <= mid && large <= best) return k256x256;
+        if (mid <= best) return k128x128;
+    }
+    if (s6 <= best) return k64x96;
+    return s4 <= best ? k64x64 : k64x32;
 }
 
 }  // namespace st

@@ -13,6 +13,11 @@ extern "C" {
 void stub_reset(void) {
     for (long long &c : g_calls) c = 0;
 }
+// The tiles of a call's product, as rows * 1000 + columns.
+int stub_linear_tile(int n, int k, int out, int num_slices, int R, int fp8) {
+    static const int kTiles[] = {16016, 16064, 32016, 32048, 48064, 64032, 64064, 64096, 128128, 256256};
+    return kTiles[st::linear_tile(n, k, out, fp8 != 0, st::linear_plan(n, out, num_slices, R).sorted)];
+}
 long long stub_calls(int kind) { return kind >= 0 && kind < kKinds ? g_calls[kind] : -1; }
 }
 

@@ -82,3 +82,12 @@ def test_linear_workspace_grows_with_every_size(L):
     for n in (1, 64, 65, 128, 256, 257):
         by_out = [size(n, 4096, out, 3, 16) for out in range(8, 40000, 8)]
         assert by_out == sorted(by_out)
+
+
+def test_shapes_are_computed_in_the_tiles_that_they_test(L):
+    import test_gpu_step_tiles as T
+    listed = T.ALL + [(256256, (fp8, *case)) for fp8 in (False, True) for case in (T.BROKEN[fp8], T.SLOTS)]
+    for tile, (fp8, n, k, widths, S, R) in listed:
+        assert L.stub_linear_tile(n, k, sum(widths), len(widths), R, int(fp8)) == tile, (tile, fp8, n, k, widths)
+    assert len({tile for tile, _ in listed}) == 10     # every kind
+    assert {tile for tile, case in T.ALL if case[0]} == {tile for tile, case in T.ALL if not case[0]}
