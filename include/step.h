@@ -52,7 +52,8 @@ enum {
  *     y             bf16, or null
  *     q, q_scale    y's e4m3 copy: q_scale[i] = max_j |y[i][j]| / 448 and
  *                   q[i][j] = y[i][j] / q_scale[i] from the unrounded y; both
- *                   null or both given.  A row of zeros gets scale 0 and q 0.
+ *                   null or both given.  A row of zeros gets scale 0 and q 0 (and
+ *                   y 0, also with eps 0).
  *                   A row that holds a NaN or an infinity gets scale NaN and q 0;
  *                   one whose squares sum past 3.4e38 gets y, scale and q 0.
  * At least one of y and q is given.  Shapes: h a multiple of 8 in [8, 32768];

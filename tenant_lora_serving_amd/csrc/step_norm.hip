@@ -118,7 +118,26 @@ __global__ __launch_bounds__(NT *ROWS) void rms_norm_kernel(NormArgs a) {
         }
     }
     row_reduce<NT>(ss, am, scratch);
-    const float rstd = 1.0f / sqrtf(ss / (float)a.h + a.eps);
+    float mean = ss / (float)a.h + a.eps;
+    float rstd = 1.0f / sqrtf(mean);
+    if (mean < 0x1p-100f) {
+        // squares below fp32's smallest numbers, and an eps that does not hide
+        // them: the row is lifted by 2^80, which keeps every s (2^-133 at
+        // least, or 0) and its square in range.  A row of zeros stays one.
+        ss = 0.0f;
+        am = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[j][i] *= 0x1p80f;
+                ss = fmaf(s[j][i], s[j][i], ss);
+                am = fmaxf(am, fabsf(s[j][i] * w[j][i]));
+            }
+        row_reduce<NT>(ss, am, scratch);
+        mean = ss / (float)a.h + a.eps * 0x1p80f * 0x1p80f;
+        rstd = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
+    }
     am *= rstd;
     if (!(ss < INFINITY)) {  // an infinity or NaN in the row, or squares past fp32
         float bad = 0.0f, big = 0.0f;

@@ -1,11 +1,14 @@
 """The serving-step operators at the edges of what they accept, against their
 definitions in 64 bits, on the GPU (tolerances as in test_gpu_step.py)."""
+import math
+
 import pytest
+import torch
 
 from tenant_lora_serving_amd import step
 from tenant_lora_serving_amd.decode_step import DecodeStep
 from test_gpu_decode_step import inputs
-from test_gpu_step import check_linear, check_score, gen, randn, tokens_for
+from test_gpu_step import BF16, E4M3, U, check_linear, check_score, gen, randn, padded, tokens_for, within
 
 pytestmark = pytest.mark.gpu
 
@@ -27,5 +30,47 @@ def test_score_workspace_of_a_larger_batch(v):
     ws = step.logprobs_workspace(600, v, 8)
     for n, top in ((600, 8), (1, 8), (37, 3), (255, 8), (511, 0), (512, 8)):
         print(f"score n={n} v={v} top={top}", flush=True)
-        z, t = randn(gen(n + v), n, v, std=3.0).bfloat16(), tokens_for(gen(n), n, v)
+        z, t = randn(gen(n + v), n, v, std=3.0).bfloat16(), padded, tokens_for, within(gen(n), n, v)
         check_score(z, t, top, step.token_logprobs(z, t, top, ws=ws))
+
+
+# ---------------------------------------------------------------- norm
+def norm_definition(x, residual, w, eps):
+    """y and the 8-bit copy's scale in 64 bits; a row of zeros is zero."""
+    s = x.double() if residual is None else x.double() + residual.double()
+    length = torch.sqrt((s * s).mean(dim=1, keepdim=True) + eps)
+    y = torch.where(s.abs().amax(dim=1, keepdim=True) > 0, s / length * w.double(), 0.0)
+    return y, y.abs().amax(dim=1) / 448
+
+
+def check_norm_eps(x, residual, w, eps):
+    y, scale = norm_definition(x, residual, w, eps)
+    r = step.rms_norm(x, w, eps, residual=residual, quant=True)
+    rel = (x.shape[1] / 64 + 32) * U
+    within(r.y, y, y.abs() * (BF16 + 2 * rel) + 1e-38, "y")
+    within(r.q_scale, scale, scale * 2 * rel + 1e-44, "q_scale")
+    live = scale > 0
+    q = torch.where(live[:, None], y / torch.where(live, scale, 1.0)[:, None], 0.0)
+    within(r.q.float(), q, q.abs() * (E4M3 + 4 * rel) + 2.0 ** -10 * (1 + 4 * rel), "q")
+    return r
+
+
+@pytest.mark.parametrize("h", [8, 1000, 4096, 20000])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -140, 1e-36, 1e-30, 1e-5])
+def test_norm_of_zero_and_tiny_rows_with_any_eps(eps, residual, h):
+    print(f"norm tiny eps={eps} residual={residual} h={h}", flush=True)
+    x = randn(gen(h), 9, h)
+    for row, power in enumerate((0, -14, -48, -52, -70, -110, -124)):
+        x[row] *= 2.0 ** power
+    x = x.bfloat16()
+    x[7] = 0
+    x[8] = 0
+    x[8, h // 2] = 2.0 ** -133           # the smallest bf16
+    res = None
+    if residual:
+        res = x.flip(1).contiguous()
+        res[7] = 0
+    w = (1 + randn(gen(1), h, std=0.1)).bfloat16()
+    r = check_norm_eps(x, res, w, eps)
+    assert (r.y[7] == 0).all() and r.q_scale[7] == 0 and (r.q.float()[7] == 0).all()
