@@ -54,8 +54,9 @@ enum {
  *                   q[i][j] = y[i][j] / q_scale[i] from the unrounded y; both
  *                   null or both given.  A row of zeros gets scale 0 and q 0 (and
  *                   y 0, also with eps 0).
- *                   A row that holds a NaN or an infinity gets scale NaN and q 0;
- *                   one whose squares sum past 3.4e38 gets y, scale and q 0.
+ *                   A row whose y holds a NaN or an infinity, from x, residual or
+ *                   weight, gets scale NaN and q 0; one whose squares sum past
+ *                   3.4e38 gets y, scale and q 0.
  * At least one of y and q is given.  Shapes: h a multiple of 8 in [8, 32768];
  * n <= 1 << 24; ldx, ldr >= h and multiples of 8; x, residual, weight,
  * residual_out and y 16-byte aligned, q 8-byte aligned; eps >= 0 and finite.

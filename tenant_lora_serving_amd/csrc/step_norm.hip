@@ -31,8 +31,10 @@ __device__ __forceinline__ float wave_sum(float v) {
     for (int d = kWave / 2; d; d >>= 1) v += __shfl_xor(v, d);
     return v;
 }
+// The larger of two magnitudes, NaN if one is (v_maximum3_f32; fmaxf would drop it).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float wave_max(float v) {
-    for (int d = kWave / 2; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    for (int d = kWave / 2; d; d >>= 1) v = larger(v, __shfl_xor(v, d));
     return v;
 }
 
@@ -50,7 +52,7 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, float2 *scratch) 
         b = 0.0f;
         for (int i = 0; i < NT / kWave; ++i) {
             a += scratch[i].x;
-            b = fmaxf(b, scratch[i].y);
+            b = larger(b, scratch[i].y);
         }
     }
 }
@@ -107,7 +109,7 @@ __global__ __launch_bounds__(NT *ROWS) void rms_norm_kernel(NormArgs a) {
         for (int i = 0; i < 8; ++i) {
             if (rr) s[j][i] += r[i];
             ss = fmaf(s[j][i], s[j][i], ss);
-            am = fmaxf(am, fabsf(s[j][i] * w[j][i]));
+            am = larger(am, fabsf(s[j][i] * w[j][i]));
         }
     }
     if (a.residual_out) {
@@ -132,25 +134,24 @@ __global__ __launch_bounds__(NT *ROWS) void rms_norm_kernel(NormArgs a) {
             for (int i = 0; i < 8; ++i) {
                 s[j][i] *= 0x1p80f;
                 ss = fmaf(s[j][i], s[j][i], ss);
-                am = fmaxf(am, fabsf(s[j][i] * w[j][i]));
+                am = larger(am, fabsf(s[j][i] * w[j][i]));
             }
         row_reduce<NT>(ss, am, scratch);
         mean = ss / (float)a.h + a.eps * 0x1p80f * 0x1p80f;
         rstd = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
     }
     am *= rstd;
-    if (!(ss < INFINITY)) {  // an infinity or NaN in the row, or squares past fp32
-        float bad = 0.0f, big = 0.0f;
+    if (!(am < INFINITY && ss < INFINITY)) {
+        // an infinity or NaN in the row or the weight, or squares or products
+        // past fp32: the maximum is taken of the results themselves
+        float none = 0.0f;
+        am = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = s[j][i] * rstd * w[j][i];
-                bad += (y != y) ? 1.0f : 0.0f;
-                big = fmaxf(big, fabsf(y));
-            }
-        row_reduce<NT>(bad, big, scratch);
-        am = bad > 0.0f ? NAN : big;
+            for (int i = 0; i < 8; ++i) am = larger(am, fabsf(s[j][i] * rstd * w[j][i]));
+        row_reduce<NT>(none, am, scratch);
+        if (!(am < INFINITY)) am = NAN;
     }
     // 1 / scale would overflow for a row whose largest |y| is below 448 / 3.4e38:
     // such a row is lifted by 2^64 first

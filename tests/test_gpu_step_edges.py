@@ -74,3 +74,31 @@ def test_norm_of_zero_and_tiny_rows_with_any_eps(eps, residual, h):
     w = (1 + randn(gen(1), h, std=0.1)).bfloat16()
     r = check_norm_eps(x, res, w, eps)
     assert (r.y[7] == 0).all() and r.q_scale[7] == 0 and (r.q.float()[7] == 0).all()
+
+
+@pytest.mark.parametrize("h", [64, 1000, 4096, 20000])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_norm_of_a_weight_that_is_not_finite(bad, h):
+    print(f"norm weight {bad} h={h}", flush=True)
+    x, w = randn(gen(h), 6, h).bfloat16(), (1 + randn(gen(1), h, std=0.1)).bfloat16()
+    x[3] = 0
+    x[4, h - 3] = 0                      # 0 times the weight is NaN, whatever the weight
+    clean, _ = norm_definition(x, None, w, 1e-5)
+    w[h - 3] = bad
+    r = step.rms_norm(x, w, 1e-5, quant=True)
+    assert r.q_scale.isnan().all() and (r.q.float() == 0).all()
+    at, rest = r.y[:, h - 3].double(), torch.arange(h, device="cuda") != h - 3
+    assert not at.isfinite().any() and at[3:5].isnan().all()
+    if not math.isnan(bad):
+        assert torch.equal(at[:3], x[:3, h - 3].double() * bad)
+    y = clean[:, rest]
+    within(r.y[:, rest], y, y.abs() * (BF16 + 2 * (h / 64 + 32) * U) + 1e-38, "the other columns")
+
+
+@pytest.mark.parametrize("h", [64, 4096, 20000])
+def test_norm_of_rows_whose_products_with_the_weight_pass_fp32(h):
+    x, w = (randn(gen(h), 4, h) * 1e15).bfloat16(), (1 + randn(gen(1), h, std=0.1)).bfloat16()
+    w[5] = 1e30                          # x w is past fp32, y is not
+    check_norm_eps(x, None, w, 1e-5)
+    x[2] = 0
+    check_norm_eps(x, None, w, 0.0)
