@@ -140,10 +140,12 @@ __global__ __launch_bounds__(NT *ROWS) void rms_norm_kernel(NormArgs a) {
         mean = ss / (float)a.h + a.eps * 0x1p80f * 0x1p80f;
         rstd = mean > 0.0f ? 1.0f / sqrtf(mean) : 0.0f;
     }
+    const bool in_range = am > 1e-30f && am < INFINITY && ss < INFINITY;
     am *= rstd;
-    if (!(am < INFINITY && ss < INFINITY)) {
-        // an infinity or NaN in the row or the weight, or squares or products
-        // past fp32: the maximum is taken of the results themselves
+    if (!in_range) {
+        // an infinity or NaN in the row or the weight, squares or products past
+        // fp32, or no product above its smallest numbers: the maximum is taken
+        // of the results themselves
         float none = 0.0f;
         am = 0.0f;
 #pragma unroll

@@ -102,3 +102,12 @@ def test_norm_of_rows_whose_products_with_the_weight_pass_fp32(h):
     check_norm_eps(x, None, w, 1e-5)
     x[2] = 0
     check_norm_eps(x, None, w, 0.0)
+
+
+@pytest.mark.parametrize("h", [64, 4096, 20000])
+@pytest.mark.parametrize("power", [-60, -96, -110])
+def test_norm_of_rows_whose_products_with_the_weight_vanish(power, h):
+    # x w is below fp32's smallest numbers, y is not
+    x = (randn(gen(h), 3, h) * 2.0 ** -45).bfloat16()
+    w = ((1 + randn(gen(1), h, std=0.1)) * 2.0 ** power).bfloat16()
+    check_norm_eps(x, None, w, 0.0)
