@@ -14,6 +14,9 @@ bool aligned(const void *p, unsigned to) { return p && (reinterpret_cast<uintptr
 bool aligned_or_null(const void *p, unsigned to) { return !p || aligned(p, to); }
 int launched(hipError_t e) { return e == hipSuccess ? STEP_OK : STEP_ELAUNCH; }
 
+// n * ld >= limit, for any ld (the product of a long stride would wrap around).
+bool spans(int n, int64_t ld, int64_t limit) { return n > 0 && (ld >= limit || n * ld >= limit); }
+
 int check_score(int n, int v, int top) {
     if (n < 0 || v < 1 || top < 0) return STEP_EINVAL;
     if (n > st::kScoreMaxRows || v > (1 << 20) || top > STEP_MAX_TOP) return STEP_EUNSUPPORTED;
@@ -75,7 +78,7 @@ int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const
     if (num_slots > st::kMaxSlots) return STEP_EUNSUPPORTED;
     if (ldx < k || ldx % 8 != 0 || ldy < out || ldy % 8 != 0) return STEP_EINVAL;
     if (xq && (ldxq < k || ldxq % 16 != 0)) return STEP_EINVAL;
-    if ((long long)n * ldx >= (1LL << 30) || (xq && (long long)n * ldxq >= (1LL << 31))) return STEP_EUNSUPPORTED;
+    if (spans(n, ldx, 1LL << 30) || (xq && spans(n, ldxq, 1LL << 31))) return STEP_EUNSUPPORTED;
     if (n == 0) return STEP_OK;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(a_pool, 16) || !aligned(b_pool, 16) || !aligned(scale, 4) ||
         !aligned(slot, 4) || !aligned(y, 16))

@@ -91,3 +91,34 @@ def test_shapes_are_computed_in_the_tiles_that_they_test(L):
         assert L.stub_linear_tile(n, k, sum(widths), len(widths), R, int(fp8)) == tile, (tile, fp8, n, k, widths)
     assert len({tile for tile, _ in listed}) == 10     # every kind
     assert {tile for tile, case in T.ALL if case[0]} == {tile for tile, case in T.ALL if not case[0]}
+
+
+def linear(L, **kw):
+    v = dict(x=0x1000, ldx=64, n=4, k=64, xq=None, ldxq=0, xs=None, w=0x2000, ws_=None, a=0x3000, b=0x4000, sc=0x5000,
+             S=3, sizes=(24, 8), R=16, slot=0x6000, y=0x7000, ldy=32, ws=0x8000, bytes=1 << 40)
+    v.update(kw)
+    sizes = (ctypes.c_int32 * len(v["sizes"]))(*v["sizes"])
+    return L.step_lora_linear(v["x"], v["ldx"], v["n"], v["k"], v["xq"], v["ldxq"], v["xs"], v["w"], v["ws_"], v["a"],
+                              v["b"], v["sc"], v["S"], len(sizes), sizes, v["R"], v["slot"], v["y"], v["ldy"],
+                              v["ws"], v["bytes"], None)
+
+
+FP8 = dict(xq=0x9000, xs=0xa000, ws_=0xb000)
+
+
+def test_linear_spans(L):
+    """Row offsets are 32-bit in the kernels: strides that pass them are refused,
+    also ones whose product with n wraps around 64 bits."""
+    for n in (1, 3, 1 << 18):
+        most = ((1 << 30) - 1) // n // 8 * 8
+        assert linear(L, n=n, ldx=most) == OK
+        most8 = ((1 << 31) - 1) // n // 16 * 16
+        assert linear(L, n=n, ldxq=most8, **FP8) == OK
+        assert L.stub_calls(LINEAR) == 2
+        for ld in (most + 8, 1 << 30, 1 << 45, 1 << 46, 1 << 47, 3 << 46, 1 << 61, (1 << 63) - 8):
+            assert linear(L, n=n, ldx=ld) == EUNSUP, (n, ld)
+        for ld in (most8 + 16, 1 << 31, 1 << 46, 1 << 47, 3 << 46, 1 << 61, (1 << 63) - 16):
+            assert linear(L, n=n, ldxq=ld, **FP8) == EUNSUP, (n, ld)
+        assert L.stub_calls(LINEAR) == 2
+        L.stub_reset()
+    assert linear(L, n=0, ldx=1 << 40) == OK and L.stub_calls(LINEAR) == 0
