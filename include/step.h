@@ -95,9 +95,10 @@ size_t step_lora_linear_workspace_bytes(int32_t n, int32_t k, int32_t out, int32
  * Limits: k a multiple of 16 in [16, 1 << 18]; every slice width a multiple
  * of 8; 1 <= num_slices <= 8; out <= 1 << 24; max_rank a multiple of 8 in
  * [8, 128]; 1 <= num_slots <= 8192; n <= 1 << 18; ldx and ldy multiples of 8
- * and ldxq of 16; n * ldx < 1 << 30, n * ldxq < 1 << 31 (STEP_EUNSUPPORTED
- * past the limits on k, out, max_rank, num_slots, n and the spans); every
- * pointer 16-byte aligned, but scales and slot 4-byte.
+ * and ldxq of 16; n * ldx < 1 << 30, n * ldxq < 1 << 31; n * out < 10^11 with
+ * xq and k <= 256 (STEP_EUNSUPPORTED past the limits on k, out, max_rank,
+ * num_slots, n and the products); every pointer 16-byte aligned, but scales
+ * and slot 4-byte.
  */
 int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const uint8_t *xq, int64_t ldxq,
                      const float *x_scale, const void *w, const float *w_scale, const uint16_t *a_pool,

@@ -78,6 +78,7 @@ int step_lora_linear(const uint16_t *x, int64_t ldx, int32_t n, int32_t k, const
     if (num_slots > st::kMaxSlots) return STEP_EUNSUPPORTED;
     if (ldx < k || ldx % 8 != 0 || ldy < out || ldy % 8 != 0) return STEP_EINVAL;
     if (xq && (ldxq < k || ldxq % 16 != 0)) return STEP_EINVAL;
+    if (xq && k <= st::kExactK && n * out >= 100000000000LL) return STEP_EUNSUPPORTED;  // (64-row tiles: the grid)
     if (spans(n, ldx, 1LL << 30) || (xq && spans(n, ldxq, 1LL << 31))) return STEP_EUNSUPPORTED;
     if (n == 0) return STEP_OK;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(a_pool, 16) || !aligned(b_pool, 16) || !aligned(scale, 4) ||

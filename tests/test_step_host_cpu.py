@@ -122,3 +122,17 @@ def test_linear_spans(L):
         assert L.stub_calls(LINEAR) == 2
         L.stub_reset()
     assert linear(L, n=0, ldx=1 << 40) == OK and L.stub_calls(LINEAR) == 0
+
+
+def test_linear_grid_of_small_tiles(L):
+    """8-bit rows of short k run in 64-row tiles only: past 10^11 results their
+    grid would pass 2^32 threads."""
+    n = 1 << 18
+    for out, want in (((10 ** 11 - 1) // n // 8 * 8, OK), (10 ** 11 // n // 8 * 8 + 8, EUNSUP), (1 << 24, EUNSUP)):
+        assert linear(L, n=n, k=16, ldxq=16, sizes=(out,), ldy=out, **FP8) == want
+        assert linear(L, n=n, k=272, ldx=272, ldxq=272, sizes=(out,), ldy=out, **FP8) == OK
+        assert linear(L, n=n, k=16, sizes=(out,), ldy=out) == OK
+        tile = L.stub_linear_tile(n, 16, out, 1, 16, 1)
+        if want == OK:
+            rows, cols = tile // 1000, tile % 1000
+            assert -(-n // rows) * (-(-out // cols) + 7) * 256 < 1 << 32
