@@ -62,6 +62,12 @@ def _check(fn: str, status: int):
         raise LoraError(fn, status, lib().step_status_string(status).decode())
 
 
+def _fits(fn: str, *sizes):
+    """Every size of the call is a 32-bit one (ctypes would hand over the low half of others)."""
+    if max(sizes) > 0x7fffffff:
+        _check(fn, -2)
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream   # what torch.cuda.current_stream() wraps, at a fortieth of its time
 
 
@@ -130,6 +136,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, *, residu
                                                             residual_out=residual_out))
     xp, ldx = _rows(x, "x", torch.bfloat16)
     n, h = x.shape
+    _fits("step_rms_norm", n, h)
     dev = _device(x, residual)
     wp = _arg(weight, "weight", torch.bfloat16, (h,), dev)
     rp, ldr, sp = None, 0, None
@@ -156,6 +163,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-5, *, residu
 # ---------------------------------------------------------------- projection
 def linear_workspace(n: int, k: int, out: int, num_slices: int, max_rank: int, device="cuda") -> torch.Tensor:
     """A workspace for calls of at most these sizes."""
+    _fits("step_lora_linear_workspace_bytes", n, k, out, num_slices, max_rank)
     b = int(lib().step_lora_linear_workspace_bytes(n, k, out, num_slices, max_rank))
     return torch.zeros(max(b, 16), dtype=torch.uint8, device=device)
 
@@ -186,6 +194,7 @@ def lora_linear(x: torch.Tensor, w: torch.Tensor, a_pool: torch.Tensor, b_pool: 
     xp, ldx = _rows(x, "x", torch.bfloat16)
     if x.shape[1] != k:
         _same("x", x.shape, (n, k))
+    _fits("step_lora_linear", n, k, N, S, L, R)
     dev = _device(x, xq, out, ws)
     sizes, total = _slice_array(tuple(slice_sizes))
     if len(sizes) != L or total != N:
@@ -231,6 +240,7 @@ class LogprobResult(NamedTuple):
 
 def logprobs_workspace(n: int, v: int, top: int = 0, device="cuda") -> torch.Tensor:
     """A workspace for calls of at most n rows, v logits a row and `top` alternatives."""
+    _fits("step_token_logprobs_workspace_bytes", n, v, top)
     b = int(lib().step_token_logprobs_workspace_bytes(n, v, top))
     return torch.zeros(max(b, 16), dtype=torch.uint8, device=device)
 
@@ -244,6 +254,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, *, 
         return _on(stream, token_logprobs, (logits, tokens, top), dict(ws=ws))
     lp, ld = _rows(logits, "logits", torch.bfloat16, torch.float32)
     n, v = logits.shape
+    _fits("step_token_logprobs", n, v, top)
     dev = _device(logits, ws)
     tp = _arg(tokens, "tokens", torch.int32, (n,), dev)
     logprob, rank = torch.empty_like(tokens, dtype=torch.float32), torch.empty_like(tokens)

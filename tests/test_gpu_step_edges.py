@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tenant_lora_serving_amd import step
+from tenant_lora_serving_amd.lora import LoraError
 from tenant_lora_serving_amd.decode_step import DecodeStep
 from test_gpu_decode_step import inputs
 from test_gpu_step import BF16, E4M3, U, check_linear, check_score, gen, randn, padded, tokens_for, within
@@ -111,3 +112,15 @@ def test_norm_of_rows_whose_products_with_the_weight_vanish(power, h):
     x = (randn(gen(h), 3, h) * 2.0 ** -45).bfloat16()
     w = ((1 + randn(gen(1), h, std=0.1)) * 2.0 ** power).bfloat16()
     check_norm_eps(x, None, w, 0.0)
+
+
+# ---------------------------------------------------------------- sizes past 32 bits
+def test_sizes_past_32_bits_are_refused():
+    far = 1 << 32                        # (17 GB, never written)
+    x = torch.empty(1, far + 64, dtype=torch.bfloat16, device="cuda")
+    token = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for call in (lambda: step.rms_norm(x, x[0], quant=True), lambda: step.token_logprobs(x, token, 2),
+                 lambda: step.token_logprobs(x[:, :100], token, far + 2)):
+        with pytest.raises(LoraError) as e:
+            call()
+        assert e.value.status == -2

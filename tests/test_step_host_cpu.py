@@ -136,3 +136,21 @@ def test_linear_grid_of_small_tiles(L):
         if want == OK:
             rows, cols = tile // 1000, tile % 1000
             assert -(-n // rows) * (-(-out // cols) + 7) * 256 < 1 << 32
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """The library takes 32-bit sizes; a larger one must not arrive there as its low half."""
+    from tenant_lora_serving_amd import step
+    from tenant_lora_serving_amd.lora import LoraError
+    if not os.path.exists(step.LIB_PATH):
+        pytest.fail("libstep.so is not built (python -m tenant_lora_serving_amd.build)")
+    far = 1 << 32
+    for sizes in ((far + 2, 100, 5), (2, far + 100, 5), (2, 100, far + 5)):
+        with pytest.raises(LoraError) as e:
+            step.logprobs_workspace(*sizes, device="cpu")
+        assert e.value.status == EUNSUP
+    for sizes in ((far + 4, 64, 32, 2, 16), (4, far + 64, 32, 2, 16), (4, 64, far + 32, 2, 16), (4, 64, 32, far + 2, 16),
+                  (4, 64, 32, 2, far + 16)):
+        with pytest.raises(LoraError) as e:
+            step.linear_workspace(*sizes, device="cpu")
+        assert e.value.status == EUNSUP
