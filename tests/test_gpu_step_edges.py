@@ -9,7 +9,7 @@ from tenant_lora_serving_amd import step
 from tenant_lora_serving_amd.lora import LoraError
 from tenant_lora_serving_amd.decode_step import DecodeStep
 from test_gpu_decode_step import inputs
-from test_gpu_step import BF16, E4M3, U, check_linear, check_score, gen, randn, padded, tokens_for, within
+from test_gpu_step import BF16, E4M3, U, check_linear, check_score, gen, randn, tokens_for, within
 
 pytestmark = pytest.mark.gpu
 
@@ -31,7 +31,7 @@ def test_score_workspace_of_a_larger_batch(v):
     ws = step.logprobs_workspace(600, v, 8)
     for n, top in ((600, 8), (1, 8), (37, 3), (255, 8), (511, 0), (512, 8)):
         print(f"score n={n} v={v} top={top}", flush=True)
-        z, t = randn(gen(n + v), n, v, std=3.0).bfloat16(), padded, tokens_for, within(gen(n), n, v)
+        z, t = randn(gen(n + v), n, v, std=3.0).bfloat16(), tokens_for(gen(n), n, v)
         check_score(z, t, top, step.token_logprobs(z, t, top, ws=ws))
 
 
