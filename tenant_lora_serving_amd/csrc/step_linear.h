@@ -78,15 +78,19 @@ __device__ __forceinline__ i32x4_t words_rsrc(const void *base, uint32_t bytes) 
                    __builtin_amdgcn_readfirstlane((int)bytes), tl::kBufWord3};
 }
 // 16 bytes a lane from the buffer into LDS at `lds` + 16 * lane; offsets past
-// the buffer write zeros.  There is no register result, so nothing is written
-// behind the compiler's back but LDS, which "memory" covers; the waits are
-// written out below.
+// the buffer write zeros.  There is no register result, so what is written is
+// m0 (the LDS address) and LDS, which "memory" covers; the waits are written
+// out below.  (m0 is a reserved register, which the compiler writes before each
+// use of its own and never keeps for us: hence the warning that is turned off.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds(i32x4_t rsrc, uint32_t off, uint32_t more, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(lds), "v"(off), "s"(rsrc), "s"(more)
-                 : "memory");
+                 : "m0", "memory");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ void barrier() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_barrier" ::: "memory");
