@@ -9,7 +9,7 @@ from tenant_lora_serving_amd import step
 from tenant_lora_serving_amd.lora import LoraError
 from tenant_lora_serving_amd.decode_step import DecodeStep
 from test_gpu_decode_step import inputs
-from test_gpu_step import BF16, E4M3, U, check_linear, check_score, gen, randn, tokens_for, within
+from test_gpu_step import BF16, E4M3, U, check_linear, check_score, gen, linear64, linear_inputs, randn, tokens_for, within
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,87 @@ def test_sizes_past_32_bits_are_refused():
         with pytest.raises(LoraError) as e:
             call()
         assert e.value.status == -2
+
+
+# ---------------------------------------------------------------- the largest sizes and spans
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,k,widths", [(4, 64, (72,)), (300, 64, (72,)), (2100, 272, (1992, 2000))])
+def test_linear_rows_as_far_apart_as_the_limit(n, k, widths, fp8):
+    print(f"linear span n={n} k={k} fp8={fp8}", flush=True)
+    args, kw = linear_inputs(n, n, k, widths, 5, 16, fp8)
+    x, rest = args[0], args[1:]
+    want = step.lora_linear(*args, **kw)
+    check_linear(args, kw, want, "close rows")
+
+    def spread(t, ld):
+        far = torch.zeros(n * ld, dtype=torch.uint8 if t.dtype == torch.float8_e4m3fn else t.dtype, device="cuda")
+        rows = far.as_strided((n, k), (ld, 1))
+        rows.copy_(t.view(torch.uint8) if t.dtype == torch.float8_e4m3fn else t)
+        return rows.view(t.dtype)
+    ldx, ldxq = ((1 << 30) - 1) // n // 8 * 8, ((1 << 31) - 1) // n // 16 * 16
+    assert torch.equal(step.lora_linear(spread(x, ldx), *rest, **kw), want)
+    if fp8:
+        kw = dict(kw, xq=spread(kw["xq"], ldxq))
+        assert torch.equal(step.lora_linear(x, *rest, **kw), want)
+    with pytest.raises(LoraError) as e:
+        step.lora_linear(x.new_zeros((n, ldx + 8))[:, :k], *rest, **kw)
+    assert e.value.status == -2
+
+
+@pytest.mark.parametrize("n", [3, 100, 300, 3000])
+def test_linear_most_slots(n):
+    print(f"linear 8192 slots n={n}", flush=True)
+    S = 8192
+    slot = torch.randint(S - 64, S, (n,), generator=gen(n), device="cuda")
+    slot[0], slot[1], slot[2] = S - 1, 0, S
+    args, kw = linear_inputs(n, n, 64, (72, 8), S, 8, slot=torch.where(slot == S, S - 1, slot))
+    check_linear(args, kw, step.lora_linear(*args), "linear")
+    past = (*args[:6], slot.int())           # S is no slot
+    check_linear(past, kw, step.lora_linear(*past), "linear")
+
+
+def whole_numbers(seed, n, k, widths, S, R, fp8):
+    """Small whole numbers, so that every sum is exact in fp32 and every result
+    the rounding of a whole number, however long the sum."""
+    g, N = gen(seed), sum(widths)
+
+    def whole(most, *shape):
+        return torch.randint(-most, most + 1, shape, generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    x, w = whole(1, n, k), whole(2, N, k)
+    slot = torch.randint(-1, S, (n,), generator=g, device="cuda").int()
+    rest = (whole(1, S, len(widths), R, k), whole(1, S, N, R), torch.ones(S, device="cuda"), widths, slot)
+    if not fp8:
+        return (x, w, *rest), {}
+    kw = dict(xq=x.to(torch.float8_e4m3fn), x_scale=torch.ones(n, device="cuda"), w_scale=torch.ones(N, device="cuda"))
+    return (x, w.to(torch.float8_e4m3fn), *rest), kw
+
+
+def check_whole(args, kw, got):
+    y, _ = linear64(args, kw)
+    assert y.abs().max() < 1 << 24 and torch.equal(got, y.float().bfloat16())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,widths", [(5, (16,)), (300, (200, 64)), (600, (1040,)), (2100, (3992,))])
+def test_linear_longest_k(n, widths, fp8):
+    print(f"linear longest k n={n} fp8={fp8}", flush=True)
+    args, kw = whole_numbers(n, n, 1 << 18, widths, 2, 8, fp8)
+    check_whole(args, kw, step.lora_linear(*args, **kw))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,k,widths", [(3, 16, ((1 << 24) - 8, 8)), (1 << 18, 16, (8,)), (1 << 18, 272, (520,))])
+def test_linear_most_columns_and_rows(n, k, widths, fp8):
+    print(f"linear largest n={n} k={k} widths={widths} fp8={fp8}", flush=True)
+    args, kw = whole_numbers(n, n, k, widths, 2, 8, fp8)
+    check_whole(args, kw, step.lora_linear(*args, **kw))
+
+
+@pytest.mark.parametrize("n,v,top", [(1 << 16, 64, 32), (1 << 16, 4200, 0), (2, 1 << 20, 32), (70, 1 << 20, 5)])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_score_most_rows_and_logits(n, v, top, fp32):
+    print(f"score largest n={n} v={v} top={top} fp32={fp32}", flush=True)
+    z = randn(gen(n + v), n, v, std=3.0)
+    z = z if fp32 else z.bfloat16()
+    t = tokens_for(gen(n), n, v)
+    check_score(z, t, top, step.token_logprobs(z, t, top))
