@@ -1,7 +1,8 @@
 // step_linear.h -- what the kernels of step_lora_linear share: the matrix
-// products of one 128-byte line of k, and the streamed product of a few rows
-// by a few weight rows, straight from memory to matrix-core registers.
-// Internal to the library.
+// products of one 128-byte line of k, loads from memory into LDS, the product
+// of a few rows by a few weight rows that a wave streams through a ring of lines
+// there, and the care that one tenant's broken adapter takes.  Internal to the
+// library.
 #pragma once
 
 #include <type_traits>
@@ -34,9 +35,9 @@ constexpr int kLine = 128;
 // instruction's 25 bits.  That is at most 2^-10 of a group's largest product,
 // and over a long k of ordinary rows 2^-15 of the result, below its rounding to
 // bf16; the exact way, the values widened to bf16, would take the bf16
-// instruction's time.  Over a short k, where a cut does not average out and the product is
-// bound by its reads, the values do go through the bf16 instruction, which
-// holds them exactly (k <= kExactK).
+// instruction's time.  Over a short k, where a cut does not average out, the
+// values do go through the bf16 instruction, which holds them exactly (k <=
+// kExactK).
 enum Form { kBf16, kE4m3, kE4m3AsBf16 };
 
 // Eight e4m3 values as bf16 (exact).

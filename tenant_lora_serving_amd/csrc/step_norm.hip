@@ -5,9 +5,11 @@
 //
 // A row is held in fp32 registers by the threads that read it, so it is read
 // once: the sum of squares and the largest |s w| are reduced together and
-// everything else is elementwise (max|y| = max|s w| * rstd).  Bound by memory
+// everything else is elementwise (max|y| = max|s w| * rstd).  Rows whose squares
+// or products leave fp32's range, or that hold a NaN or an infinity, take
+// another reduction.  Bound by memory
 // traffic when there are many rows (6947 x 4096 with residual, both outputs:
-// 40 us, 6.4 TB/s of the least bytes) and by the latency of one load, one
+// 41 us, 6.2 TB/s of the least bytes) and by the latency of one load, one
 // reduction and one store when there are few (1 x 4096: 2.8 us).
 #include "common.h"
 #include "step_kernels.h"
