@@ -147,7 +147,9 @@ struct Inner {
     const uint16_t *xab;
 };
 
-// The 8-bit form's scales: lane m holds row m's, columns from c0.
+// The 8-bit form's scales: lane m holds row m's, columns from c0.  (One after
+// the other, as in the large tiles: the product of two small scales may be no
+// fp32 number where the result is one.)
 template <int MT, int NT>
 __device__ __forceinline__ void apply_scales(const LinearArgs &a, float my_scale, int c0, int cols,
                                              f32x4_t (&acc)[NT][MT]) {
@@ -166,7 +168,7 @@ __device__ __forceinline__ void apply_scales(const LinearArgs &a, float my_scale
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][i][e] *= xs * ws[j][e];
+            for (int e = 0; e < 4; ++e) acc[j][i][e] = acc[j][i][e] * xs * ws[j][e];
     }
 }
 

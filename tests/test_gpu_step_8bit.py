@@ -62,3 +62,29 @@ def test_one_product_dominates(n, N, k, cancel):
     if k > 256:
         tol = tol + cut_bound(kw["xq"], kw["x_scale"], args[1], kw["w_scale"])
     within(step.lora_linear(*args, **kw), y, tol, "linear")
+
+
+@pytest.mark.parametrize("n,N", [(1, 64), (40, 200), (200, 520), (1000, 3080), (2100, 3992)])
+@pytest.mark.parametrize("k", [256, 272])
+@pytest.mark.parametrize("power", [-124, -60, 90])
+def test_scales_whose_product_leaves_fp32(power, k, n, N):
+    """x_scale * w_scale may be a subnormal, or none at all, where the results are
+    ordinary numbers (smallest step of bf16: 2^-133)."""
+    print(f"8-bit scales n={n} N={N} k={k} power={power}", flush=True)
+    g = gen(n + k)
+    x, w = randn(g, n, k), randn(g, N, k, std=k ** -0.5)
+    xs, ws = x.abs().amax(dim=1) / 448, w.abs().amax(dim=1) / 448
+    xq, wq = (x / xs[:, None]).to(torch.float8_e4m3fn), (w / ws[:, None]).to(torch.float8_e4m3fn)
+    xs = xs * 2.0 ** power
+    if power == -60:
+        ws = ws * 2.0 ** -60
+    if power == 90:
+        ws = ws * 2.0 ** -100
+    kw = dict(xq=xq, x_scale=xs, w_scale=ws)
+    none = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    args = (x.bfloat16(), wq, torch.zeros(1, 1, 8, k, device="cuda").bfloat16(),
+            torch.zeros(1, N, 8, device="cuda").bfloat16(), torch.ones(1, device="cuda"), (N,), none)
+    y, tol = linear64(args, kw)
+    if k > 256:
+        tol = tol + cut_bound(xq, xs, wq, ws)
+    within(step.lora_linear(*args, **kw), y, tol + 2.0 ** -134 + 2.0 ** -149, "linear")
