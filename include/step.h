@@ -1,8 +1,9 @@
 /*
  * step.h -- C ABI of the operators a serving step runs around the routed LoRA
  * delta on MI355X (gfx950): the norm in front of a projection, the shared
- * projection with every request's adapter added to it, and the log
- * probabilities of the answered tokens.  Library: libstep.so.
+ * projection with every request's adapter added to it, the paged cache of keys
+ * and values with the attention that reads it, and the log probabilities of the
+ * answered tokens.  Library: libstep.so.
  *
  * Conventions, the same as lora.h's:
  *  - bf16 values travel as uint16_t bit patterns, e4m3 (OCP, no infinities,
@@ -138,6 +139,93 @@ size_t step_token_logprobs_workspace_bytes(int32_t n, int32_t v, int32_t top);
 int step_token_logprobs(const void *logits, int64_t ld, int32_t fp32, int32_t n, int32_t v, const int32_t *tokens,
                         int32_t top, float *logprob, int32_t *rank, float *entropy, int32_t *top_ids,
                         float *top_logprobs, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The paged cache of keys and values: two arrays of the same shape [pages][page]
+ * [kv_heads][dim] and the same strides (page_stride, token_stride and
+ * head_stride, in elements; dim is contiguous), in bf16 or, with k_scale and
+ * v_scale ([kv_heads], float, at least 0), in e4m3, a stored value times its
+ * head's scale being the value.  A token's place is page number * page + place
+ * in the page.  dim is a multiple of 16 in [16, 256]; heads a multiple of
+ * kv_heads, at most 64 times and at most 4096; strides multiples of 8 (of 16 in
+ * e4m3), at least dim, and free where the axis has length 1; both arrays 16-byte
+ * aligned; pages * page < 1 << 31.
+ */
+
+/* The most tokens of a call, and the most requests and prefixes. */
+#define STEP_MAX_TOKENS (1 << 20)
+#define STEP_MAX_REQUESTS (1 << 16)
+
+/*
+ * Tokens' keys and values into the cache, the keys and the queries turned by
+ * their positions' angles on the way.  For token t with row
+ * (cos_0 .. cos_{rot/2-1}, sin_0 .. sin_{rot/2-1}) of rotation at positions[t],
+ * in every head of q and k and for i < rot / 2
+ *     (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i)
+ * where (a, b) are the columns (i, i + rot / 2) or, with neighbours != 0,
+ * (2 i, 2 i + 1); columns from rot on stay as they are.  In fp32, rounded once.
+ *    q      [n][ldq], heads * dim used columns, or null with q_out
+ *    k, v   [n][ldk], [n][ldv], kv_heads * dim used columns
+ *    positions [n], rotation [rotation_rows][rot] (not read with rot == 0)
+ *    place  [n]; a token whose place is not in the cache is not stored
+ *    q_out  [n][ldo]; may be q itself (then ldo == ldq)
+ * In e4m3 a value over its head's scale is rounded to nearest, and to +-448 where
+ * it is larger.  A position outside the rotation makes the token's q NaN, and the
+ * token is not stored.  Where two tokens have one place, each 16 values (8 in
+ * bf16) of it are one of the two's.  Limits: n <= STEP_MAX_TOKENS; rot a multiple
+ * of 16, at most dim; leading dimensions multiples of 8; q, k, v, q_out and
+ * rotation 16-byte aligned.
+ */
+int step_kv_append(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                   int32_t n, int32_t heads, int32_t kv_heads, int32_t dim, const int32_t *positions,
+                   const float *rotation, int32_t rotation_rows, int32_t rot, int32_t neighbours, const int32_t *place,
+                   void *k_cache, void *v_cache, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                   int32_t pages, int32_t page, const float *k_scale, const float *v_scale, uint16_t *q_out,
+                   int64_t ldo, void *stream);
+
+/* Workspace bytes step_paged_attention needs (0 for a shape that it refuses).
+ * They serve every call of the same heads and dim with at most n rows, with
+ * prefixes only if prefixes > 0 here.  Of this workspace only the first
+ * STEP_ATTENTION_ZEROED bytes need the zero fill. */
+#define STEP_ATTENTION_ZEROED 4096
+size_t step_paged_attention_workspace_bytes(int32_t n, int32_t heads, int32_t kv_heads, int32_t dim,
+                                            int32_t prefixes);
+
+/*
+ * Attention of a batch of requests over the paged cache.  Request b has the
+ * rows starts[b] .. starts[b + 1] of q (row b alone without starts) and its keys
+ * 0 .. lens[b], key j in place j % page of page table[b][j / page].  For row i
+ * and head h, with the keys and values of head h / (heads / kv_heads),
+ *     out[i][h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q[i][h] k_j)
+ *     lse[i][h] = ln sum_j p_j                                  (if not null)
+ * over the request's keys; with causal != 0 the request's rows are its last
+ * tokens, so the t-th of r rows sees keys j <= lens[b] - r + t.
+ * Prefixes: the requests prefix_starts[p] .. prefix_starts[p + 1] share the
+ * prefix_lens[p] keys on the pages prefix_table[p], which all their rows see
+ * before their own keys; requests before the first group and behind the last
+ * have no prefix.  Each prefix is read once for all its requests.
+ *    q [n][ldq], out [n][ldo], heads * dim used columns; lse [n][heads]
+ *    starts [requests + 1] and prefix_starts [prefixes + 1] ascending
+ *    max_rows   the most rows of a request; it decides only which kernel runs
+ * Rows that belong to no request stay as they are.  A row without keys gets 0
+ * and lse -infinity.  Keys on a page number that the cache does not have count as
+ * absent, lengths end with the table.  Keys whose score is -infinity are absent
+ * too; an infinity or NaN reaches no row that does not see its key.  Products in
+ * bf16 with fp32 sums, p rounded to bf16 before its product with v, one rounding
+ * of the result; the order of the sums goes by the lengths of the whole batch,
+ * and by nothing else.
+ * Limits: n <= STEP_MAX_TOKENS; requests, prefixes <= STEP_MAX_REQUESTS;
+ * table_cols * page and prefix_cols * page <= 1 << 24; leading dimensions of q
+ * and out multiples of 8; q, out and ws 16-byte aligned; scale > 0 and finite.
+ */
+int step_paged_attention(const uint16_t *q, int64_t ldq, int32_t n, int32_t requests, int32_t heads, int32_t kv_heads,
+                         int32_t dim, const void *k_cache, const void *v_cache, int64_t page_stride,
+                         int64_t token_stride, int64_t head_stride, int32_t pages, int32_t page, const float *k_scale,
+                         const float *v_scale, const int32_t *table, int64_t ld_table, int32_t table_cols,
+                         const int32_t *lens, const int32_t *starts, int32_t max_rows, int32_t causal, float scale,
+                         int32_t prefixes, const int32_t *prefix_table, int64_t ld_prefix_table, int32_t prefix_cols,
+                         const int32_t *prefix_lens, const int32_t *prefix_starts, uint16_t *out, int64_t ldo,
+                         float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /* A static, human-readable name for a status code. */
 const char *step_status_string(int status);

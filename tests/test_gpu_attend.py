@@ -1,0 +1,456 @@
+"""Attention over the paged cache against its 64-bit definition.
+
+The bound of a result: its own rounding to bf16 (2^-8 of it), p's rounding to bf16 before the
+product (2^-8 of every term, so at most 2^-8 sum p |v|), and fp32 on the way: a score of `dim`
+products is off by at most dim 2^-24 times the sum of their magnitudes, which p and the sum
+of p take over as a relative error, the exponential and its argument by some 2^-20, sums over
+`keys` by keys 2^-24."""
+import math
+import random
+
+import pytest
+import torch
+
+from tenant_lora_serving_amd import step
+from tenant_lora_serving_amd.lora import LoraError
+
+pytestmark = pytest.mark.gpu
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+class Batch:
+    """Requests with `rows[b]` rows and `lens[b]` keys, groups of them with shared prefixes, over a
+    cache whose every place that holds no key is NaN."""
+
+    def __init__(self, seed, rows, lens, heads=8, kv=2, dim=128, page=16, cache="bf16", layout="apart", prefixes=(),
+                 first=0, decode=False, pad=0, std=1.0, more_cols=0):
+        g = self.g = gen(seed)
+        self.rows, self.lens, self.prefixes, self.first = rows, lens, prefixes, first   # prefixes: (length, requests)
+        self.heads, self.kv, self.dim, self.page = heads, kv, dim, page
+        n = sum(rows)
+        spans = list(lens) + [p for p, _ in prefixes]
+        counts = [-(-x // page) for x in spans]
+        total = sum(counts) + 3
+        order = torch.randperm(total, generator=torch.Generator().manual_seed(seed)).tolist()
+        shape = {"apart": (2, total, page, kv, dim), "heads": (2, total, kv, page, dim),
+                 "joint": (total, 2, page, kv, dim)}[layout]
+        pool = torch.randn(shape, generator=g, device="cuda")
+        kc, vc = {"apart": lambda t: (t[0], t[1]), "joint": lambda t: (t[:, 0], t[:, 1]),
+                  "heads": lambda t: (t[0].transpose(1, 2), t[1].transpose(1, 2))}[layout](pool)
+        held = torch.zeros(total, page, dtype=torch.bool, device="cuda")
+        tables, at = [], 0
+        for x, c in zip(spans, counts):
+            tables.append(order[at:at + c])
+            at += c
+            for i, p in enumerate(tables[-1]):
+                held[p, :min(page, x - i * page)] = True
+        self.k_scale = self.v_scale = None
+        if cache == "e4m3":
+            self.k_scale, self.v_scale = 0.5 + torch.rand(2, kv, generator=g, device="cuda")
+            kc.mul_(100), vc.mul_(100)
+            kc.clamp_(-448, 448), vc.clamp_(-448, 448)
+            self.k_scale, self.v_scale = self.k_scale / 100, self.v_scale / 100
+        kc[~held], vc[~held] = math.nan, math.nan
+        self.pool = pool.to(torch.float8_e4m3fn if cache == "e4m3" else torch.bfloat16)
+        self.k_cache, self.v_cache = {"apart": lambda t: (t[0], t[1]), "joint": lambda t: (t[:, 0], t[:, 1]),
+                                      "heads": lambda t: (t[0].transpose(1, 2), t[1].transpose(1, 2))}[layout](self.pool)
+        own, pre = tables[:len(lens)], tables[len(lens):]
+        wide = max([len(t) for t in own] + [1]) + more_cols
+        self.pages = ints([t + [-1] * (wide - len(t)) for t in own])
+        self.len_t = ints(list(lens))
+        self.starts = None if decode else ints([sum(rows[:b]) for b in range(len(rows) + 1)])
+        self.prefix = None
+        if prefixes:
+            wide = max(max(len(t) for t in pre), 1)
+            ends = [first + sum(r for _, r in prefixes[:i]) for i in range(len(prefixes) + 1)]
+            self.prefix = step.Prefixes(ints([t + [-1] * (wide - len(t)) for t in pre]), ints([p for p, _ in prefixes]),
+                                        ints(ends))
+        q = torch.randn(n, heads * dim + pad, generator=g, device="cuda") * std
+        self.q = q.bfloat16()[:, :heads * dim].unflatten(1, (heads, dim))
+
+    def call(self, **kw):
+        a = dict(starts=self.starts, prefix=self.prefix, k_scale=self.k_scale, v_scale=self.v_scale, lse=True,
+                 max_rows=max(self.rows, default=1) or 1)
+        a.update(kw)
+        return step.paged_attention(a.pop("q", self.q), self.k_cache, self.v_cache, a.pop("pages", self.pages),
+                                    a.pop("lens", self.len_t), **a)
+
+    def read(self, cache, scale, table, length):
+        j = torch.arange(length, device="cuda")
+        at = table.long()[j // self.page]
+        bad = (at < 0) | (at >= cache.shape[0])
+        raw = cache.view(torch.uint8) if cache.dtype == torch.float8_e4m3fn else cache
+        x = raw[at.clamp(0, cache.shape[0] - 1), j % self.page].view(cache.dtype).double()
+        if scale is not None:
+            x = x * scale.double()[None, :, None]
+        return x, bad
+
+    def want(self, causal=True, scale=None, pages=None, lens=None):
+        """(out, lse, bound of out, bound of lse) in 64 bits."""
+        pages = self.pages if pages is None else pages
+        scale = self.dim ** -0.5 if scale is None else scale
+        n, heads, dim = self.q.shape
+        out = torch.zeros(n, heads, dim, dtype=torch.float64, device="cuda")
+        lse = torch.full((n, heads), -math.inf, dtype=torch.float64, device="cuda")
+        tol, tol_lse = torch.zeros_like(out), torch.zeros_like(lse)
+        group = [-1] * len(self.lens)
+        at = self.first
+        for p, (_, r) in enumerate(self.prefixes):
+            group[at:at + r] = [p] * r
+            at += r
+        r0 = 0
+        for b, rows in enumerate(self.rows):
+            length = self.lens[b] if lens is None else lens[b]
+            length = min(max(length, 0), pages.shape[1] * self.page)
+            k, bad = self.read(self.k_cache, self.k_scale, pages[b], length)
+            v, _ = self.read(self.v_cache, self.v_scale, pages[b], length)
+            j, t = torch.arange(length, device="cuda"), torch.arange(rows, device="cuda")
+            see = j[None, :] <= (length - rows + t[:, None] if causal else length)
+            see = see & ~bad[None, :]
+            if group[b] >= 0:
+                pl = self.prefixes[group[b]][0]
+                pk, pbad = self.read(self.k_cache, self.k_scale, self.prefix.pages[group[b]], pl)
+                pv, _ = self.read(self.v_cache, self.v_scale, self.prefix.pages[group[b]], pl)
+                k, v = torch.cat([pk, k]), torch.cat([pv, v])
+                see = torch.cat([(~pbad)[None, :].expand(rows, pl), see], dim=1)
+            q = self.q[r0:r0 + rows].double()
+            if rows and k.shape[0]:
+                for h in range(heads):
+                    kh, vh = k[:, h // (heads // self.kv)], v[:, h // (heads // self.kv)]
+                    s = torch.where(see, q[:, h] @ kh.T * scale, -math.inf)
+                    some = see.any(dim=1, keepdim=True)
+                    m = torch.where(some, s.amax(dim=1, keepdim=True), 0.0)
+                    p = torch.where(see, torch.exp(s - m), 0.0)
+                    total = p.sum(dim=1, keepdim=True)
+                    p = p / torch.where(total == 0, 1.0, total)
+                    # (what a row does not see must not reach it, be it NaN)
+                    free = torch.isfinite(vh).all()
+                    vf = torch.where(torch.isfinite(vh), vh, 0.0)
+                    o = p @ vf
+                    if not free:
+                        for key in (~torch.isfinite(vh).all(dim=1)).nonzero()[:, 0].tolist():
+                            o += torch.where(see[:, key, None], torch.where(torch.isfinite(vh[key]), 0.0, vh[key])[None], 0.0)
+                    out[r0:r0 + rows, h] = o
+                    lse[r0:r0 + rows, h] = torch.where(some, m + total.log(), -math.inf)[:, 0]
+                    mag = torch.where(see, q[:, h].abs() @ torch.where(torch.isfinite(kh), kh, 0.0).abs().T * scale, 0.0)
+                    e = (mag.amax(dim=1, keepdim=True) * (dim + 2) + k.shape[0] + 16) * 2.0 ** -24 + 2.0 ** -20
+                    tol[r0:r0 + rows, h] = 2.0 ** -8 * o.abs() + (p @ vf.abs()) * (1.01 * 2.0 ** -8 + 4 * e) + 1e-30
+                    tol_lse[r0:r0 + rows, h] = 2 * e[:, 0] + lse[r0:r0 + rows, h].abs() * 2.0 ** -22
+            r0 += rows
+        return out, lse, tol, tol_lse
+
+
+def near(got, want, tol, what):
+    got = got.double()
+    same = torch.isnan(got) == torch.isnan(want)
+    assert same.all(), f"{what}: {(~same).sum()} of {same.numel()} are NaN on one side only, first {(~same).nonzero()[0].tolist()}"
+    fine = torch.isfinite(want)
+    inf = torch.isinf(want)
+    assert torch.equal(got[inf], want[inf]), f"{what}: infinities differ"
+    over = ((got - want).abs() > tol) & fine
+    if over.any():
+        at = over.nonzero()[0].tolist()
+        raise AssertionError(f"{what}: {over.sum()} of {over.numel()} off, first {at}: {got[tuple(at)].item()} for "
+                             f"{want[tuple(at)].item()}, bound {tol[tuple(at)].item()}")
+
+
+def check(b, what="", causal=True, scale=None, want=None, **kw):
+    r = b.call(causal=causal, scale=scale, **kw)
+    lens = kw["lens"].tolist() if "lens" in kw else None
+    out, lse, tol, tol_lse = want or b.want(causal, scale, kw.get("pages"), lens)
+    near(r.out, out, tol, f"{what} out")
+    if r.lse is not None:
+        near(r.lse, lse, torch.where(torch.isfinite(tol_lse), tol_lse, 0.0), f"{what} lse")
+    return r
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 700, 1500]
+
+
+@pytest.mark.parametrize("dim", [16, 64, 80, 112, 128, 208, 256])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_tokens(dim, cache):
+    check(Batch(1, [1] * len(LENS), LENS, dim=dim, cache=cache, decode=True), f"{dim} {cache}")
+
+
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 256])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows(dim, cache, causal):
+    rows = [1, 0, 130, 33, 7, 64, 5, 200]
+    lens = [1, 40, 130, 300, 3, 65, 0, 517]
+    check(Batch(2, rows, lens, dim=dim, cache=cache), f"{dim} {cache}", causal=causal)
+
+
+@pytest.mark.parametrize("heads,kv", [(1, 1), (3, 1), (5, 5), (6, 2), (16, 1), (12, 4), (15, 3), (17, 1), (34, 2), (48, 1), (64, 1)])
+@pytest.mark.parametrize("decode", [True, False])
+def test_heads(heads, kv, decode):
+    lens = [5, 333, 64, 0, 1000]
+    rows = [1] * 5 if decode else [5, 40, 64, 2, 9]
+    check(Batch(3, rows, lens, heads=heads, kv=kv, dim=64, decode=decode), f"{heads}/{kv}")
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 24, 100, 128, 2048])
+@pytest.mark.parametrize("layout", ["apart", "joint", "heads"])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_pages_and_layouts(page, layout, cache):
+    lens = [1, 50, 129, 517]
+    check(Batch(4, [1] * 4, lens, page=page, layout=layout, cache=cache, decode=True, pad=16, more_cols=3), "tokens")
+    check(Batch(5, [1, 50, 100, 37], lens, page=page, layout=layout, cache=cache, pad=48), "rows")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_shared_prefixes(dim, cache):
+    """Groups of one and of many requests, prefixes of no key, requests without prefix on both sides."""
+    n = 60
+    lens = [(7 * i) % 90 for i in range(n)]
+    groups = ((1, 1), (700, 40), (0, 3), (33, 2), (129, 9))
+    check(Batch(6, [1] * n, lens, dim=dim, cache=cache, prefixes=groups, first=2, decode=True), "tokens")
+    rows = [(5 * i) % 13 for i in range(n)]
+    check(Batch(7, rows, [x + r for x, r in zip(lens, rows)], dim=dim, cache=cache, prefixes=groups, first=2), "rows")
+    check(Batch(8, rows, lens, dim=dim, cache=cache, prefixes=groups, first=5), "rows that pass their keys")
+
+
+def test_prefix_of_everything():
+    check(Batch(9, [1] * 33, [3] * 33, prefixes=((5000, 33),), decode=True), "one prefix")
+    check(Batch(10, [1] * 3, [0] * 3, prefixes=((5000, 3),), decode=True), "nothing of their own")
+    check(Batch(11, [1], [1], prefixes=((1, 1),), decode=True), "a key each")
+    check(Batch(12, [300, 200], [300, 900], prefixes=((2000, 2),)), "prompts")
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_long_and_short(cache):
+    """One long request beside short ones: its tiles are cut and joined."""
+    check(Batch(13, [1] * 40, [20000] + [50] * 39, cache=cache, decode=True), "tokens")
+    check(Batch(14, [20] + [1] * 9, [30000] + [50] * 9, cache=cache), "few rows at the end of many keys")
+    check(Batch(15, [1], [9999], heads=32, kv=8, cache=cache, decode=True), "one request")
+    check(Batch(16, [700], [5000], heads=4, kv=1, cache=cache), "a piece of a prompt")
+    check(Batch(17, [16, 3], [12000, 9000], heads=1, kv=1, dim=256, cache=cache), "one head")
+
+
+def test_many_requests():
+    rng = random.Random(3)
+    n = 1000
+    check(Batch(18, [1] * n, [rng.choice([0, 1, rng.randint(0, 80)]) for _ in range(n)], heads=2, kv=1, dim=64, decode=True),
+          "tokens")
+    rows = [rng.choice([0, 1, 2, 9]) for _ in range(n)]
+    check(Batch(19, rows, [r + rng.randint(0, 40) for r in rows], heads=2, kv=2, dim=64), "rows")
+
+
+def test_rows_that_see_nothing():
+    """More rows than keys: the first ones see none of the request's."""
+    b = Batch(20, [50, 9, 4, 130], [10, 0, 4, 2])
+    r = check(b, "rows")
+    assert (r.out[:40] == 0).all() and (r.lse[:40] == -math.inf).all() and (r.out[50:59] == 0).all()
+    b = Batch(21, [3, 2], [1, 0], heads=4, kv=1)
+    r = check(b, "few rows")
+    assert (r.out[:2] == 0).all()
+
+
+def test_loud_and_quiet_scores():
+    for std in (0.0, 1e-3, 30.0, 1000.0):
+        check(Batch(22, [1] * 5, [1, 40, 300, 600, 33], std=std, decode=True), f"tokens {std}")
+        check(Batch(23, [20, 3, 130], [40, 300, 600], std=std), f"rows {std}")
+    check(Batch(24, [1] * 3, [100, 40, 300], decode=True), "scale", scale=0.7)
+    check(Batch(25, [30] * 3, [100, 40, 300]), "scale", scale=1e-4)
+    b = Batch(26, [1, 40], [100, 300], cache="e4m3")   # a head whose keys were all zeros has scale 0
+    b.k_scale[1] = 0.0
+    check(b, "scale 0 of a head")
+
+
+# ---------------------------------------------------------------- what is masked
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,lens", [([60, 9], [60, 200]), ([4, 2], [40, 130])])
+def test_infinities_behind_a_row(cache, rows, lens):
+    """A token's NaN or infinite key and value reach it and later tokens, none before."""
+    def place(b, request, j):
+        return b.pages[request, j // b.page].item(), j % b.page
+    for which in ("k", "v", "both"):
+        b = Batch(30, rows, lens, heads=4, kv=1, cache=cache)
+        for request, j, value in ((0, lens[0] - 2, math.nan), (1, lens[1] - 1, math.inf)):
+            if cache == "e4m3":
+                value = math.nan
+            p, t = place(b, request, j)
+            if which in ("k", "both"):
+                b.k_cache[p, t, 0, 5] = value
+            if which in ("v", "both"):
+                b.v_cache[p, t, 0, 7] = value
+                b.v_cache[p, t, 0, 100] = -value
+        r = b.call()
+        if which == "v":
+            check(b, which)
+        seen = [rows[0] - 2, rows[0] + rows[1] - 1]
+        assert torch.isfinite(r.out[:seen[0]]).all() and torch.isfinite(r.out[rows[0]:seen[1]]).all()
+        assert not torch.isfinite(r.out[seen[0]:rows[0]]).all() and not torch.isfinite(r.out[seen[1]]).all()
+
+
+def test_pages_that_are_not_there():
+    """Keys on page numbers outside the cache are absent; tables may be shorter than lengths."""
+    for decode in (True, False):
+        b = Batch(31, [1] * 3 if decode else [20, 40, 9], [100, 300, 64], decode=decode)
+        pages = b.pages.clone()
+        pages[0, 2] = -1
+        pages[1, 0], pages[1, 17] = b.k_cache.shape[0], 2 ** 31 - 1
+        pages[2, :] = -2 ** 31
+        r = check(b, "absent", pages=pages)
+        assert (r.out[-1] == 0).all()
+        check(b, "short table", pages=b.pages[:, :3].contiguous())
+        check(b, "strided table", pages=b.pages[:, :3])
+        check(b, "longer than the table", lens=ints([100, 2 ** 31 - 1, 64]), pages=b.pages[:, :6])
+        check(b, "negative", lens=ints([-5, -2 ** 31, 64]))
+    b = Batch(32, [1] * 2, [5, 5], decode=True)
+    r = b.call(pages=b.pages[:, :0])
+    assert (r.out == 0).all() and (r.lse == -math.inf).all()
+
+
+def test_starts_that_make_no_sense_stay_inside():
+    b = Batch(33, [20, 40, 9], [100, 300, 64])
+    out = torch.full((b.q.shape[0] + 8, 8, 128), 7.0, device="cuda", dtype=torch.bfloat16)
+    for starts in ([0, -5, 2 ** 31 - 1, 3], [50, 40, 30, 20], [-1, -1, -1, -1], [69, 1000, 69, 1000]):
+        b.call(starts=ints(starts), out=out[4:-4])
+        assert (out[:4] == 7).all() and (out[-4:] == 7).all()
+    b = Batch(34, [1] * 9, [40] * 9, prefixes=((50, 4), (20, 3)), decode=True)
+    for ends in ([0, -5, 100], [9, 5, 1], [-1, -1, 2 ** 31 - 1]):
+        b.call(prefix=b.prefix._replace(starts=ints(ends)))
+
+
+# ---------------------------------------------------------------- buffers
+def test_rows_of_no_request_stay():
+    b = Batch(35, [5, 0, 30], [50, 3, 30])
+    q = torch.cat([b.q, b.q[:9]])
+    out = torch.full((q.shape[0], 8, 160), 3.0, device="cuda", dtype=torch.bfloat16)[:, :, :128]
+    with pytest.raises(ValueError):
+        b.call(q=q, out=out)                      # heads that are not side by side
+    out = torch.full((q.shape[0], 8 * 128 + 24), 3.0, device="cuda", dtype=torch.bfloat16)
+    r = b.call(q=q, out=out[:, :1024].unflatten(1, (8, 128)))
+    want = b.want()
+    near(r.out[:35], want[0], want[2], "out")
+    assert (out[35:] == 3).all() and (out[:, 1024:] == 3).all()
+    starts = b.starts + 4                          # and before the first
+    out.fill_(3.0)
+    q = torch.cat([b.q[:4], b.q])
+    r = b.call(q=q, out=out[:39, :1024].unflatten(1, (8, 128)), starts=starts)
+    near(r.out[4:], want[0], want[2], "out")
+    assert (out[:4] == 3).all() and (out[39:] == 3).all()
+
+
+def test_a_wrong_hint_changes_nothing_but_time():
+    b = Batch(36, [40, 3], [100, 200], heads=4, kv=2)
+    for hint in (1, 2, 40, 10 ** 6, None):
+        check(b, f"hint {hint}", max_rows=hint)
+
+
+def test_one_workspace_for_every_size():
+    ws = step.attention_workspace(400, 8, 2, 128, prefixes=True)
+    ws[4096:] = 0x7f                               # (its rest may hold anything)
+    for seed, rows, lens, groups in ((40, [1] * 30, [3000] + [10] * 29, ((900, 12),)), (41, [300, 100], [5000, 100], ()),
+                                     (42, [1], [4000], ()), (43, [9, 200], [2000, 3000], ((4000, 2),))):
+        b = Batch(seed, rows, lens, prefixes=groups)
+        for _ in range(2):
+            check(b, f"{seed}", ws=ws)
+    assert (ws[:4096] == 0).all()
+    with pytest.raises(LoraError):
+        Batch(44, [1], [5], prefixes=((5, 1),)).call(ws=step.attention_workspace(1, 8, 2, 128))
+
+
+def test_the_same_bits_every_time():
+    for b in (Batch(45, [1] * 30, [3000] + [300] * 29, prefixes=((900, 12),), decode=True), Batch(46, [300, 100], [5000, 100])):
+        first = b.call()
+        for _ in range(5):
+            again = b.call()
+            assert torch.equal(first.out, again.out) and torch.equal(first.lse, again.lse)
+
+
+def test_streams_and_two_calls_at_once():
+    b, c = Batch(47, [1] * 30, [3000] + [300] * 29, decode=True), Batch(48, [300, 100], [5000, 100], prefixes=((500, 2),))
+    want_b, want_c = b.call(), c.call()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got_b, got_c = b.call(stream=s), c.call(stream=t)
+        torch.cuda.synchronize()
+        assert torch.equal(got_b.out, want_b.out) and torch.equal(got_c.out, want_c.out)
+
+
+def test_graph_follows_lengths_and_tables():
+    """A captured call replayed with other lengths, pages, queries and prefixes."""
+    for decode in (True, False):
+        rows = [1] * 12 if decode else [5, 0, 70, 1, 30, 2, 2, 2, 40, 1, 1, 9]
+        lens = [50, 900, 80, 10, 4000, 2, 77, 300, 41, 1, 1000, 64]
+        groups = ((300, 5), (700, 4))
+        b = Batch(50, rows, lens, prefixes=groups, first=1, decode=decode, more_cols=100)
+        ws = step.attention_workspace(sum(rows), 8, 2, 128, prefixes=True)
+        b.call(ws=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = b.call(ws=ws)
+        for i in range(4):
+            order = torch.randperm(12, generator=torch.Generator().manual_seed(i)).tolist()
+            c = Batch(51 + i, rows, [lens[k] for k in order], prefixes=groups, first=1, decode=decode)
+            wide = c.pages.shape[1]
+            b.pages.fill_(-1)
+            b.pages[:, :wide] = c.pages
+            b.len_t.copy_(c.len_t)
+            b.q.copy_(c.q)
+            b.k_cache[:c.k_cache.shape[0]].copy_(c.k_cache[:b.k_cache.shape[0]])
+            b.v_cache[:c.v_cache.shape[0]].copy_(c.v_cache[:b.v_cache.shape[0]])
+            for x, y in zip(b.prefix, c.prefix):
+                x.copy_(y)
+            graph.replay()
+            torch.cuda.synchronize()
+            b.lens = c.lens
+            want = b.want()
+            near(held.out, want[0], want[2], f"replay {i}")
+            again = b.call(ws=ws)
+            assert torch.equal(held.out, again.out) and torch.equal(held.lse, again.lse)
+
+
+def test_a_cache_past_32_bits():
+    """Pages that begin past 2^31 elements and past 2^32 bytes."""
+    b = Batch(60, [1, 1], [100, 40], heads=2, kv=1, decode=True)
+    far = torch.empty(2 ** 31 + 2 ** 24, dtype=torch.bfloat16, device="cuda")
+    total = b.k_cache.shape[0]
+    stride = (2 ** 31) // (total - 1) // 8 * 8
+    kc = far.as_strided(b.k_cache.shape, (stride, 128, 128, 1))
+    kc.copy_(b.k_cache)
+    vc = far.as_strided(b.v_cache.shape, (stride, 128, 128, 1), 2 ** 20)
+    vc.copy_(b.v_cache)
+    want = b.want()
+    b.k_cache, b.v_cache = kc, vc
+    check(b, "far", want=want)
+
+
+def test_refusals():
+    b = Batch(61, [1, 1], [10, 20], cache="e4m3", decode=True)
+    c = Batch(62, [3, 2], [10, 20])
+    for kw in (dict(k_scale=None), dict(v_scale=None), dict(k_scale=b.k_scale[:1]), dict(pages=b.pages[:1]),
+               dict(q=b.q[:1]), dict(out=torch.empty(3, 8, 128, device="cuda", dtype=torch.bfloat16)),
+               dict(lens=b.len_t[:1]), dict(prefix=step.Prefixes(b.pages, b.len_t, b.len_t))):
+        with pytest.raises(ValueError):
+            b.call(**kw)
+    for kw in (dict(q=b.q.float()), dict(pages=b.pages.long()), dict(lens=b.len_t.cpu()), dict(starts=torch.zeros(3))):
+        with pytest.raises(TypeError):
+            b.call(**kw)
+    with pytest.raises((TypeError, ValueError)):   # (another device and another type)
+        b.call(ws=torch.zeros(9))
+    for kw in (dict(scale=0.0), dict(scale=math.nan), dict(ws=torch.zeros(4096, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(LoraError):
+            b.call(**kw)
+    with pytest.raises(ValueError):
+        c.call(k_scale=b.k_scale, v_scale=b.v_scale)
+    with pytest.raises(ValueError):
+        c.call(starts=c.starts[:2])
+    with pytest.raises(ValueError):
+        step.paged_attention(b.q, b.k_cache, b.v_cache[:, :8], b.pages, b.len_t, k_scale=b.k_scale, v_scale=b.v_scale)
+    with pytest.raises(LoraError):   # rows whose heads do not share evenly
+        step.paged_attention(b.q[:, :3].contiguous(), b.k_cache, b.v_cache, b.pages, b.len_t, k_scale=b.k_scale, v_scale=b.v_scale)
+    r = b.call(q=b.q[:0], pages=b.pages[:0], lens=b.len_t[:0])
+    assert r.out.shape == (0, 8, 128) and r.lse.shape == (0, 8)
