@@ -148,8 +148,8 @@ int step_token_logprobs(const void *logits, int64_t ld, int32_t fp32, int32_t n,
  * head's scale being the value.  A token's place is page number * page + place
  * in the page.  dim is a multiple of 16 in [16, 256]; heads a multiple of
  * kv_heads, at most 64 times and at most 4096; strides multiples of 8 (of 16 in
- * e4m3), at least dim, and free where the axis has length 1; both arrays 16-byte
- * aligned; pages * page < 1 << 31.
+ * e4m3), at least dim, below 1 << 35, and free where the axis has length 1; both
+ * arrays 16-byte aligned; pages * page < 1 << 31.
  */
 
 /* The most tokens of a call, and the most requests and prefixes. */

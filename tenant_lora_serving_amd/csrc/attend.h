@@ -74,7 +74,6 @@ __device__ __forceinline__ float only_not_finite(float v) { return fabsf(v) < IN
 // acc += four values of a key where they are not finite.
 __device__ __forceinline__ void add_not_finite(float *acc, uint2 v, bool seen) {
     const float f[4] = {tl::bf_lo(v.x), tl::bf_hi(v.x), tl::bf_lo(v.y), tl::bf_hi(v.y)};
-#pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] += seen ? only_not_finite(f[e]) : 0.0f;
 }
 
@@ -107,6 +106,12 @@ __device__ __forceinline__ int64_t job_cost(const AttendArgs &a, Span s, int tok
     return tiles_cost(s, tokens, a.causal, tiles_of(s.rows, tokens));
 }
 
+// Neighbouring ranges, which share keys, go to one XCD.
+__device__ __forceinline__ int workgroup_of(const AttendArgs &a) {
+    const int groups = a.groups_of_threads, blk = blockIdx.x;
+    return groups % 8 == 0 ? (blk % 8) * (groups / 8) + blk / 8 : blk;
+}
+
 struct Found {
     int64_t wave_sum[kWaves], base;
     int job;
@@ -124,9 +129,7 @@ struct Walk {
     __device__ __forceinline__ bool find(const AttendArgs &a, int rows, int least, int whole, Found &found) {
         const int tid = threadIdx.x, lane = tl::lane_id();
         tokens = rows / a.each;
-        // neighbouring ranges, which share keys, on one XCD
-        const int groups = a.groups_of_threads, blk = blockIdx.x;
-        w = groups % 8 == 0 ? (blk % 8) * (groups / 8) + blk / 8 : blk;
+        w = workgroup_of(a);
         const int per = (a.jobs + kThreads - 1) / kThreads, j0 = min(tid * per, a.jobs), j1 = min(j0 + per, a.jobs);
         int64_t mine = 0;
         for (int k = j0; k < j1; ++k) mine += a.kv * job_cost(a, job_of(a, k).s, tokens);
@@ -143,7 +146,7 @@ struct Walk {
             total += found.wave_sum[k];
         }
         total = scalar64(total);
-        r = ranges_of(total, groups, least, whole);
+        r = ranges_of(total, a.groups_of_threads, least, whole);
         const int64_t begin = w * r.size;
         end = begin + r.size < total ? begin + r.size : total;
         if (begin >= total) return false;
@@ -200,12 +203,10 @@ struct TileRows {
 };
 
 // ---------------------------------------------------------------- keys in the cache
-// Byte offset of key `key`'s token in the cache, or -1 if its page is none.
-template <int SIZE>
-__device__ __forceinline__ int64_t token_offset(const AttendArgs &a, int page, int in_page) {
-    return ((uint32_t)page < (uint32_t)a.cache.pages)
-               ? (page * a.cache.page_stride + in_page * a.cache.token_stride) * SIZE
-               : -1;
+// Byte offset of a token in the cache.  (Strides are whole 16-byte units, of
+// which less than 2^32 make one.)
+__device__ __forceinline__ uint64_t token_offset(const AttendArgs &a, int page, int in_page) {
+    return ((uint64_t)(uint32_t)page * a.page_units + (uint64_t)(uint32_t)in_page * a.token_units) * 16;
 }
 
 // ---------------------------------------------------------------- results of pieces

@@ -14,7 +14,7 @@ bool aligned(const void *p, unsigned to) { return p && (reinterpret_cast<uintptr
 bool aligned_or_null(const void *p, unsigned to) { return !p || aligned(p, to); }
 int launched(hipError_t e) { return e == hipSuccess ? STEP_OK : STEP_ELAUNCH; }
 
-constexpr int64_t kMostStride = 1LL << 40;
+constexpr int64_t kMostStride = 1LL << 40, kMostCacheStride = 1LL << 35;  // (the latter in 16 bytes: 32 bits)
 constexpr int kMostKeys = 1 << 24;
 
 int check_heads(int n, int heads, int kv, int dim) {
@@ -38,25 +38,26 @@ int check_cache(st::CacheArgs &c, int kv, int dim) {
     for (auto &x : axes) {
         if (x.size == 1) x.stride = 0;
         else if (x.stride < dim || x.stride % unit != 0) return STEP_EINVAL;
-        else if (x.stride >= kMostStride) return STEP_EUNSUPPORTED;
+        else if (x.stride >= kMostCacheStride) return STEP_EUNSUPPORTED;
     }
     return STEP_OK;
 }
 
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// What an attention's workspace holds: tickets, what the rows bring from their
-// prefixes, results of pieces.
+// What an attention's workspace holds: tickets, notes of split tiles, what the
+// rows bring from their prefixes, results of pieces.
 struct AttendPlan {
-    size_t state, sums, pieces, total;
+    size_t joins, state, sums, pieces, total;
 };
-int few_groups(int dim) { return dim <= 64 ? 768 : dim <= 128 ? 512 : 256; }
-int many_groups(int dim) { return dim <= 128 ? 512 : 256; }
+int few_groups(int dim) { return dim <= 64 ? st::kFewGroups : dim <= 128 ? 512 : 256; }
+int many_groups(int dim) { return dim <= 128 ? st::kManyGroups : 256; }
 AttendPlan attend_plan(int n, int heads, int dim, bool prefixes) {
     AttendPlan p{};
     const size_t rows = (size_t)n * heads, few = few_groups(dim) * st::piece_floats(st::kFewRows, dim),
                  many = many_groups(dim) * st::piece_floats(st::kManyRows, dim);
-    p.state = st::kTicketBytes;
+    p.joins = st::kTicketBytes;
+    p.state = p.joins + up256(st::kManyGroups * sizeof(st::Join));
     p.sums = p.state + (prefixes ? up256(rows * 2 * sizeof(float)) : 0);
     p.pieces = p.sums + (prefixes ? up256(rows * st::padded_dim(dim) * sizeof(float)) : 0);
     p.total = p.pieces + up256(2 * (few > many ? few : many) * sizeof(float));
@@ -162,6 +163,9 @@ int step_paged_attention(const uint16_t *q, int64_t ldq, int32_t n, int32_t requ
     a.dim = dim;
     a.scale = scale * 1.44269504088896340736f;
     a.cache = c;
+    const int unit = k_scale ? 16 : 8;
+    a.page_units = (uint32_t)(c.page_stride / unit);
+    a.token_units = (uint32_t)(c.token_stride / unit);
     a.div = st::page_div(page);
     a.requests = requests;
     a.starts = starts;
@@ -170,6 +174,8 @@ int step_paged_attention(const uint16_t *q, int64_t ldq, int32_t n, int32_t requ
     a.lse = lse;
     char *const base = static_cast<char *>(ws);
     a.tickets = reinterpret_cast<int32_t *>(base);
+    a.zeros = base + st::kZerosAt;
+    a.joins = reinterpret_cast<st::Join *>(base + plan.joins);
     a.pieces = reinterpret_cast<float *>(base + plan.pieces);
     const hipStream_t on = static_cast<hipStream_t>(stream);
     st::AttendArgs own = a;

@@ -170,7 +170,9 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_few_kernel(A
         };
         auto offset_at = [&](int k0, int page) {
             const int key = k0 + lane % 32;
-            return token_offset<kSize>(a, page, key - page_of(a.div, key) * a.cache.page);
+            return (uint32_t)page < (uint32_t)a.cache.pages
+                       ? (int64_t)token_offset(a, page, key - page_of(a.div, key) * a.cache.page)
+                       : -1;
         };
         u32x4_t kr[kLoads], vr[kLoads];
         uint32_t there = 0;  // keys of the 32 in registers that are in the cache
@@ -276,9 +278,10 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_few_kernel(A
                 for (int key = 0; key < kKeys; ++key)
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
-                        float *const to = reinterpret_cast<float *>(&acc[j]);
-                        add_not_finite(to, *reinterpret_cast<const uint2 *>(lv + key * Sh::kV + 32 * j + 8 * h),
+                        float x[4] = {};
+                        add_not_finite(x, *reinterpret_cast<const uint2 *>(lv + key * Sh::kV + 32 * j + 8 * h),
                                        k0 + key < seen);
+                        acc[j] += f32x4_t{x[0], x[1], x[2], x[3]};
                     }
             }
             wave_sync();

@@ -38,8 +38,8 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t st);
 // keys that its last row sees.  All tiles' costs one after another, request by
 // request, key head by key head, are cut into equal ranges, one for every
 // workgroup.  A tile that costs more than `whole` is cut where the ranges
-// meet, its pieces' results go to the workspace and whoever finishes last
-// joins them; a smaller one belongs to the workgroup that its middle falls to.
+// meet, and its pieces' results go to the workspace and are joined; a smaller
+// one belongs to the workgroup that its middle falls to.
 // Everything follows from the lengths, so the device divides by itself and a
 // captured call follows lengths that change.
 constexpr int kTileCost = 64;
@@ -127,11 +127,15 @@ __host__ __device__ inline int piece_slot(const Ranges &r, int w, int64_t at) { 
 constexpr int kFewRows = 16, kManyRows = 128;  // rows of a tile: of few rows, of many
 constexpr int kMaxEach = 64;                   // query heads of a key head
 constexpr int kMaxDim = 256;
-constexpr int kFewGroups = 1024, kManyGroups = 512;  // workgroups at most
+constexpr int kFewGroups = 768, kManyGroups = 512;  // workgroups at most
 constexpr int kFewLeast = 128, kManyLeast = 128;     // the least range of one
 constexpr int kFewWhole = 256, kManyWhole = 1024;    // a tile of no more is not cut
 constexpr int kFewStep = 128, kManyStep = 64;        // keys of a round
-constexpr size_t kTicketBytes = kFewGroups * sizeof(int32_t);
+constexpr int kJoinGroups = 512;                     // workgroups that join pieces of many rows
+// A workspace begins with a ticket for every workgroup, 0 between calls, and 16
+// bytes of zeros.
+constexpr size_t kTicketBytes = 4096, kZerosAt = kTicketBytes - 16;
+static_assert(kFewGroups * sizeof(int32_t) <= kZerosAt && kManyGroups <= kFewGroups, "a ticket a workgroup");
 
 // key / page for keys below 2^24: (key * mul) >> shift.
 struct PageDiv {
@@ -145,14 +149,20 @@ __host__ __device__ inline PageDiv page_div(int page) {
 }
 __host__ __device__ inline int page_of(PageDiv d, int key) { return (int)(((uint64_t)(uint32_t)key * d.mul) >> d.shift); }
 
-// A row's softmax on the way: its maximum (times log2 e), sum, and weighted sum of values.
+// A split tile of many rows: how many pieces, where the first one's results
+// are (those of the next workgroups' in their first slots), its rows and key head.
+struct Join {
+    int pieces, slot, row, rows, g, unused[3];
+};
 struct AttendArgs {
     const uint16_t *q;
     int64_t ldq;
     int n, kv, each, dim;
     float scale;  // times log2 e
     CacheArgs cache;
+    uint32_t page_units, token_units;  // strides in 16 bytes
     PageDiv div;
+    const char *zeros;  // 16 bytes
     // The jobs: request j has rows starts[j] .. starts[j + 1] (row j alone
     // without starts) and lens[j] keys on the pages of row j of the table.
     // With groups, job j is the rows of the requests groups[j - 1] ..
@@ -171,7 +181,8 @@ struct AttendArgs {
     int64_t ldo;
     float *lse;
     // the pieces of split tiles
-    int32_t *tickets;
+    int32_t *tickets;  // few rows: whoever takes the last ticket joins them
+    Join *joins;       // many rows: a launch of its own does
     float *pieces;
     int groups_of_threads;
 };

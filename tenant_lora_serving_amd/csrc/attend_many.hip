@@ -6,9 +6,9 @@
 //     o = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c q k_j - m),   c = scale log2 e
 //
 // in one pass over the keys with the running maximum m and sum.  Bound by the
-// matrix cores and the exponentials.  Each of the four waves holds 32 rows; all
-// read the keys and values from LDS, two buffers in turn, the next 64 keys on
-// their way through registers meanwhile, one barrier a round.
+// matrix cores, the exponentials and LDS reads.  Each of the four waves holds 32
+// rows; all read the keys and values from LDS, two buffers in turn, the next 64
+// keys on their way meanwhile, one barrier a round.
 //
 // S^T = K Q^T gives a lane one row of q and half of the keys, and p as it lies
 // there is the operand that O^T = V^T P^T wants, with the keys of the product
@@ -32,16 +32,33 @@ __device__ __forceinline__ f32x16_t mfma_32x32x16(const u32x4_t a, const u32x4_t
 }
 
 constexpr int kKeys = kManyStep;
+// Rows of keys lie side by side, 16-byte chunk c of key j at place c ^ k_turn(j)
+// or c ^ v_turn(j): 16 keys' reads of one chunk of K, and 4 keys' reads of 64
+// bytes of V, then fall on different banks.
 template <int D>
 struct ManyShared {
-    // (16 bytes between rows of K, 32 between rows of V against bank conflicts)
-    static constexpr int kK = 2 * D + 16, kV = 2 * D + 32;
-    char k[2][kKeys * kK], v[2][kKeys * kV];
-    uint64_t there[2][kWaves];  // keys that are in the cache
-    int broken[2];              // 1 + the first key of a tile with values that are not finite
+    static constexpr int kRow = 2 * D;
+    char k[2][kKeys * kRow], v[2][kKeys * kRow];
+    uint64_t absent[2][kWaves];  // keys whose page the cache does not have
     Found found;
-    int last;
+    static __device__ __forceinline__ int k_turn(int key) { return key & (D == 64 ? 7 : 15); }
+    static __device__ __forceinline__ int v_turn(int key) {
+        return D == 64 ? (key & 2) << 1 : (key & 3) << 2 | (key & 4) >> 1;
+    }
 };
+
+// 16 bytes a lane from memory into LDS at `lds` + 16 * lane.  There is no
+// register result, so what is written is m0 (the LDS address) and LDS, which
+// "memory" covers; the wait is written out where the data is needed.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_lds(const char *p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p) : "m0", "memory");
+}
+#pragma clang diagnostic pop
+__device__ __forceinline__ uint32_t lds_address(const char *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
 
 // What a lane holds of its row: maximum, sum (of its half of the keys on the
 // way), and columns 32 j + 8 (i / 4) + 4 h + i % 4 of the weighted sum.
@@ -51,58 +68,52 @@ struct RowState {
     f32x16_t o[D / 32];
 };
 
-template <int D>
-__device__ __forceinline__ void many_results(const AttendArgs &a, const Walk &w, const RowState<D> &x, int64_t row,
-                                             int qh, int h) {
+// Four columns of a row's result, or of what it leaves for its next keys.
+__device__ __forceinline__ void put_columns(const AttendArgs &a, int64_t row, int qh, int dim, int c, float f,
+                                            const f32x4_t o) {
+    if (a.sums_out)
+        *reinterpret_cast<f32x4_t *>(a.sums_out + (row * (a.kv * a.each) + qh) * dim + c) = o;
+    else if (c < a.dim)
+        *reinterpret_cast<uint2 *>(a.out + row * a.ldo + qh * a.dim + c) =
+            make_uint2(tl::pack_bf16x2(o[0] * f, o[1] * f), tl::pack_bf16x2(o[2] * f, o[3] * f));
+}
+__device__ __forceinline__ void put_stats(const AttendArgs &a, int64_t row, int qh, float m, float l) {
     const int64_t rh = row * (a.kv * a.each) + qh;
-    if (a.state_out) {
-        if (h == 0) *reinterpret_cast<float2 *>(a.state_out + 2 * rh) = make_float2(x.m, x.l);
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4_t *>(a.sums_out + rh * D + 32 * j + 8 * i + 4 * h) =
-                    f32x4_t{x.o[j][4 * i], x.o[j][4 * i + 1], x.o[j][4 * i + 2], x.o[j][4 * i + 3]};
-        return;
-    }
-    const float vs = a.cache.v_scale ? a.cache.v_scale[w.g] : 1.0f, f = x.l == 0.0f ? 0.0f : vs / x.l;
-    uint16_t *const to = a.out + row * a.ldo + qh * a.dim;
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = 32 * j + 8 * i + 4 * h;
-            if (c < a.dim)
-                *reinterpret_cast<uint2 *>(to + c) =
-                    make_uint2(tl::pack_bf16x2(x.o[j][4 * i] * f, x.o[j][4 * i + 1] * f),
-                               tl::pack_bf16x2(x.o[j][4 * i + 2] * f, x.o[j][4 * i + 3] * f));
-        }
-    if (h == 0 && a.lse) a.lse[rh] = x.l == 0.0f ? -INFINITY : (base_of(x.m) + log2f(x.l)) * kLn2;
+    if (a.state_out)
+        *reinterpret_cast<float2 *>(a.state_out + 2 * rh) = make_float2(m, l);
+    else if (a.lse)
+        a.lse[rh] = l == 0.0f ? -INFINITY : (base_of(m) + log2f(l)) * kLn2;
+}
+__device__ __forceinline__ float result_factor(const AttendArgs &a, int g, float l) {
+    return l == 0.0f ? 0.0f : (a.cache.v_scale ? a.cache.v_scale[g] : 1.0f) / l;
 }
 
-// Pieces' results lie as the lanes hold them.
+// Pieces' results lie as the lanes hold them: pair i of a lane's columns, then the rows' maxima and sums.
 template <int D>
-__device__ __forceinline__ float *piece_sums(const AttendArgs &a, int slot, int wave, int pair) {
-    return a.pieces + (int64_t)slot * (kManyRows * (D + 2)) + ((wave * (D / 4) + pair) * kWave + tl::lane_id()) * 2;
+__device__ __forceinline__ float2 *piece_sums(const AttendArgs &a, int slot, int wave, int pair) {
+    return reinterpret_cast<float2 *>(a.pieces + (int64_t)slot * (kManyRows * (D + 2))) +
+           (wave * (D / 4) + pair) * kWave + tl::lane_id();
 }
 template <int D>
-__device__ __forceinline__ float *piece_stats(const AttendArgs &a, int slot, int wave) {
-    return a.pieces + (int64_t)slot * (kManyRows * (D + 2)) + kManyRows * D + (wave * 32 + tl::lane_id() % 32) * 2;
+__device__ __forceinline__ float2 *piece_stats(const AttendArgs &a, int slot, int wave) {
+    return reinterpret_cast<float2 *>(a.pieces + (int64_t)slot * (kManyRows * (D + 2)) + kManyRows * D) + wave * 32 +
+           tl::lane_id() % 32;
 }
 
 template <int D, bool F8>
 __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
     using Sh = ManyShared<D>;
     constexpr int kSize = F8 ? 1 : 2;
-    constexpr int kLanes = D * kSize / 16, kRows = kThreads / kLanes, kLoads = kKeys / kRows;  // of a key; keys of a load
+    constexpr int kLanes = D * kSize / 16, kOfWave = kWave / kLanes;  // lanes of a key; keys of a wave's load
+    constexpr int kLoads = kKeys / (kWaves * kOfWave);
     __shared__ Sh sh;
     Walk w;
-    if (threadIdx.x < 2) sh.broken[threadIdx.x] = 0;
+    if (threadIdx.x == 0) a.joins[workgroup_of(a)].pieces = 0;
     if (!w.find(a, kManyRows, kManyLeast, kManyWhole, sh.found)) return;
-    const int tid = threadIdx.x, lane = tl::lane_id(), wave = scalar(tl::wave_id()), h = lane / 32;
-    const int lc = tid % kLanes, lr = tid / kLanes;  // this thread's chunk and key of a load
-    const bool in_dim = lc < a.dim * kSize / 16;
-    const int64_t chunk = in_dim ? lc * 16 : 0;
+    const int lane = tl::lane_id(), wave = scalar(tl::wave_id()), h = lane / 32;
+    // this lane's key of load u is (u * kWaves + wave) * kOfWave + lr
+    const int lc = lane % kLanes, lr = lane / kLanes;
+    auto key_of = [&](int u) { return (u * kWaves + wave) * kOfWave + lr; };
     const char *const kc = static_cast<const char *>(a.cache.k), *const vc = static_cast<const char *>(a.cache.v);
     do {
         const int keys = w.keys(a);
@@ -110,7 +121,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
         if (!p.mine) continue;
         const TileRows t(a, w);
         const int32_t *const table = table_of(a, w.j);
-        const int64_t head = w.g * a.cache.head_stride * kSize + chunk;
+        const int64_t head = w.g * a.cache.head_stride * kSize;
         const char *const kh = kc + head, *const vh = vc + head;
         // this lane's row of q
         const int r = wave * 32 + lane % 32, r_first = wave * 32, r_last = min(r_first + 31, t.count - 1);
@@ -119,7 +130,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
         const int64_t row = t.row0 + token;
         const int qh = w.g * a.each + (live ? r % a.each : 0);
         const int seen = live ? TileRows::seen(a, w.job.s, token) : 0;
-        const int all_see = TileRows::seen(a, w.job.s, t.first);  // the tile's rows
+        // the keys that some of the wave's rows see, and that all do
         const int wave_sees = any ? TileRows::seen(a, w.job.s, t.first + r_last / a.each) : 0;
         const int wave_all_see = TileRows::seen(a, w.job.s, t.first + r_first / a.each);
         u32x4_t q[D / 16];
@@ -150,190 +161,263 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
                     }
         }
 
-        u32x4_t kr[kLoads], vr[kLoads];
-        int page[kLoads];
-        bool there[kLoads];
+        u32x4_t kr[F8 ? kLoads : 1], vr[F8 ? kLoads : 1];
+        int page[kLoads], in_page[kLoads];
         auto pages = [&](int k0) {
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
-                const int key = k0 + u * kRows + lr;
-                page[u] = key < p.hi ? table[page_of(a.div, key)] : -1;
+                const int key = k0 + key_of(u), at = page_of(a.div, key);
+                in_page[u] = key - at * a.cache.page;
+                page[u] = key < p.hi ? table[at] : -1;
             }
         };
-        auto start = [&](int k0) {
+        // Chunks of absent keys and past the head's columns are read from zeros:
+        // their scores are masked, but an infinity or NaN among their values
+        // would make NaN of p = 0.
+        auto start = [&](int k0, int buf) {
+            uint64_t absent = 0;
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
-                const int key = k0 + u * kRows + lr;
-                const int64_t off = token_offset<kSize>(a, page[u], key - page_of(a.div, key) * a.cache.page);
-                there[u] = off >= 0;
-                const int64_t o = off >= 0 ? off : 0;
-                kr[u] = tl::ld16(kh + o);
-                vr[u] = tl::ld16(vh + o);
-            }
-        };
-        auto store = [&](int k0, int buf) {
-            bool broken = false;
-            uint64_t ok = 0;
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const int key = u * kRows + lr;
-                if (!in_dim) kr[u] = tl::zero4();
-                // (values of absent keys meet p = 0, which an infinity or NaN there would turn into NaN)
-                if (!there[u]) vr[u] = tl::zero4();
-                // one bit a key, from the first of its lanes
-                uint64_t bits = __ballot(there[u]);
-                constexpr int kOfWave = kWave / kLanes;  // keys of a wave's load
-                uint64_t mine = 0;
-#pragma unroll
-                for (int e = 0; e < kOfWave; ++e) mine |= ((bits >> (e * kLanes)) & 1) << e;
-                ok |= mine << (u * kRows + wave * kOfWave);
-                char *const ks = sh.k[buf] + key * Sh::kK, *const vs = sh.v[buf] + key * Sh::kV;
+                const bool there = (uint32_t)page[u] < (uint32_t)a.cache.pages;
+                if (__any(!there)) {  // one bit a key, from the first of its lanes
+                    const uint64_t bits = __ballot(!there);
+                    for (int e = 0; e < kOfWave; ++e)
+                        absent |= ((bits >> (e * kLanes)) & 1) << ((u * kWaves + wave) * kOfWave + e);
+                }
+                const uint64_t off = token_offset(a, page[u], in_page[u]);
                 if constexpr (F8) {
-                    const u32x4_t v0 = widen8(vr[u].x, vr[u].y), v1 = widen8(vr[u].z, vr[u].w);
-                    tl::st16(ks + lc * 32, widen8(kr[u].x, kr[u].y));
-                    tl::st16(ks + lc * 32 + 16, widen8(kr[u].z, kr[u].w));
-                    tl::st16(vs + lc * 32, v0);
-                    tl::st16(vs + lc * 32 + 16, v1);
-                    if (k0 + kKeys > all_see) broken |= not_finite(v0) || not_finite(v1);
+                    const bool read = there && lc < a.dim / 16;
+                    kr[u] = tl::ld16(read ? kh + off + lc * 16 : a.zeros);
+                    vr[u] = tl::ld16(read ? vh + off + lc * 16 : a.zeros);
                 } else {
-                    tl::st16(ks + lc * 16, kr[u]);
-                    tl::st16(vs + lc * 16, vr[u]);
-                    if (k0 + kKeys > all_see) broken |= not_finite(vr[u]);
+                    // (the place is the lane's, the chunk that belongs there comes from the turn)
+                    const int key = key_of(u), ck = lc ^ Sh::k_turn(key), cv = lc ^ Sh::v_turn(key);
+                    const int at = (u * kWaves + wave) * kWave * 16;
+                    load_lds(there && ck < a.dim / 8 ? kh + off + ck * 16 : a.zeros, lds_address(sh.k[buf]) + at);
+                    load_lds(there && cv < a.dim / 8 ? vh + off + cv * 16 : a.zeros, lds_address(sh.v[buf]) + at);
                 }
             }
-            if (lane == 0) sh.there[buf][wave] = ok;
-            if (broken) sh.broken[buf] = k0 + 1;
+            if (lane == 0) sh.absent[buf][wave] = absent;
+        };
+        auto store = [&](int buf) {
+            if constexpr (F8) {
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int key = key_of(u), tk = Sh::k_turn(key), tv = Sh::v_turn(key);
+                    char *const ks = sh.k[buf] + key * Sh::kRow, *const vs = sh.v[buf] + key * Sh::kRow;
+                    tl::st16(ks + ((2 * lc) ^ tk) * 16, widen8(kr[u].x, kr[u].y));
+                    tl::st16(ks + ((2 * lc + 1) ^ tk) * 16, widen8(kr[u].z, kr[u].w));
+                    tl::st16(vs + ((2 * lc) ^ tv) * 16, widen8(vr[u].x, vr[u].y));
+                    tl::st16(vs + ((2 * lc + 1) ^ tv) * 16, widen8(vr[u].z, vr[u].w));
+                }
+            }
+        };
+        auto round = [&](int k0, int buf, auto masked) {
+            f32x16_t s[2] = {};
+            const char *const lk = sh.k[buf] + lane % 32 * Sh::kRow;
+            const int tk = Sh::k_turn(lane % 32);  // (key 32 more has the same)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    s[b] = mfma_32x32x16(tl::ld16(lk + 32 * b * Sh::kRow + ((2 * kk + h) ^ tk) * 16), q[kk], s[b]);
+            if constexpr (decltype(masked)::value) {
+                uint64_t absent = 0;
+                for (int k = 0; k < kWaves; ++k) absent |= sh.absent[buf][k];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int key = 32 * b + 8 * (i / 4) + 4 * h + i % 4;
+                        if (k0 + key >= seen || ((absent >> key) & 1)) s[b][i] = -INFINITY;
+                    }
+            }
+            float big = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+            for (int i = 1; i < 16; ++i) big = fmaxf(big, fmaxf(s[0][i], s[1][i]));
+            big = fmaxf(big, __shfl_xor(big, 32));
+            // The sums stay relative to an older maximum until a score passes it by
+            // 2^8: p may be that large as well, and scaling the sums costs as much
+            // as a quarter of a product.
+            const float m2 = fmaxf(x.m, big * cf);
+            if (__any(m2 > x.m + 8.0f)) {
+                const float f = exp2_fast(x.m - base_of(m2));
+                x.m = m2;
+                x.l *= f;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) x.o[j] *= f;
+            }
+            const float base = base_of(x.m);
+            u32x4_t pk[4];
+            float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {  // 16 keys each
+                float pr[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) pr[i] = exp2_fast(fmaf(s[c / 2][8 * (c % 2) + i], cf, -base));
+                l0 += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+                l1 += (pr[4] + pr[5]) + (pr[6] + pr[7]);
+                pk[c] = u32x4_t{tl::pack_bf16x2(pr[0], pr[1]), tl::pack_bf16x2(pr[2], pr[3]),
+                                tl::pack_bf16x2(pr[4], pr[5]), tl::pack_bf16x2(pr[6], pr[7])};
+            }
+            x.l += l0 + l1;
+            // keys 16 c + 4 h + lane % 16 / 4 and 8 more, columns 32 j + 16 (lane / 16 % 2) + 4 (lane % 4) .. of V
+            const int vkey = 4 * h + lane % 16 / 4;
+            const char *const lv = sh.v[buf] + vkey * Sh::kRow + lane % 2 * 8;
+            const int tv = Sh::v_turn(vkey), vchunk = lane / 16 % 2 * 2 + lane % 4 / 2;
+            auto values = [&](int c, int j) {  // (key 8 more has the same turn)
+                const char *const at = lv + 16 * c * Sh::kRow + ((4 * j + vchunk) ^ tv) * 16;
+                const uint2 lo = read_transposed(at), hi = read_transposed(at + 8 * Sh::kRow);
+                return u32x4_t{lo.x, lo.y, hi.x, hi.y};
+            };
+            bool broken = false;
+            if constexpr (decltype(masked)::value) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) broken |= not_finite(values(c, j));
+                broken = __any(broken);
+                asm volatile("" ::: "memory");  // (read again below, not kept in registers)
+            }
+            if (!broken) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) x.o[j] = mfma_32x32x16(values(c, j), pk[c], x.o[j]);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {
+                        u32x4_t v = values(c, j);
+                        for (int e = 0; e < 4; ++e) v[e] = drop_not_finite(v[e]);
+                        x.o[j] = mfma_32x32x16(v, pk[c], x.o[j]);
+                    }
+#pragma unroll 1
+                for (int key = 0; key < kKeys; ++key) {
+                    const char *const at = sh.v[buf] + key * Sh::kRow + 8 * h;
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(at + ((4 * j + i) ^ Sh::v_turn(key)) * 16);
+                            float f[4] = {};
+                            add_not_finite(f, v, k0 + key < seen);
+                            for (int e = 0; e < 4; ++e) x.o[j][4 * i + e] += f[e];
+                        }
+                }
+            }
         };
         if (p.lo < p.hi) {
             pages(p.lo);
-            start(p.lo);
+            start(p.lo, 0);
             pages(p.lo + kKeys);
-            store(p.lo, 0);
-            __syncthreads();
+            store(0);
         }
         int buf = 0;
 #pragma unroll 1
         for (int k0 = p.lo; k0 < p.hi; k0 += kKeys, buf ^= 1) {
-            if (k0 + kKeys < p.hi) {
-                start(k0 + kKeys);
+            if constexpr (!F8) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            const bool more = k0 + kKeys < p.hi;
+            if (more) {
+                start(k0 + kKeys, buf ^ 1);
                 pages(k0 + 2 * kKeys);
             }
-            if (any && k0 < wave_sees) {
-                const char *const lk = sh.k[buf] + (lane % 32) * Sh::kK + 16 * h;
-                f32x16_t s[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    s[b] = f32x16_t{};
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        s[b] = mfma_32x32x16(tl::ld16(lk + 32 * b * Sh::kK + 32 * kk), q[kk], s[b]);
-                }
-                uint64_t ok = 0;
-                for (int k = 0; k < kWaves; ++k) ok |= sh.there[buf][k];
-                if (k0 + kKeys > wave_all_see || ok != ~0ull) {
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int key = 32 * b + 8 * (i / 4) + 4 * h + i % 4;
-                            if (k0 + key >= seen || !((ok >> key) & 1)) s[b][i] = -INFINITY;
-                        }
-                }
-                float big = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) big = fmaxf(big, fmaxf(s[0][i], s[1][i]));
-                big = fmaxf(big, __shfl_xor(big, 32));
-                const float m2 = fmaxf(x.m, big * cf), base = base_of(m2), f = exp2_fast(x.m - base);
-                x.m = m2;
-                x.l *= f;
-                u32x4_t pk[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {  // 16 keys each
-                    float pr[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        pr[i] = exp2_fast(fmaf(s[c / 2][8 * (c % 2) + i], cf, -base));
-                        x.l += pr[i];
-                    }
-                    pk[c] = u32x4_t{tl::pack_bf16x2(pr[0], pr[1]), tl::pack_bf16x2(pr[2], pr[3]),
-                                    tl::pack_bf16x2(pr[4], pr[5]), tl::pack_bf16x2(pr[6], pr[7])};
-                }
-                const char *const lv =
-                    sh.v[buf] + (4 * h + lane % 16 / 4) * Sh::kV + (lane / 16 % 2) * 32 + lane % 4 * 8;
-                auto add = [&](auto care) {
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) {
-                        x.o[j] *= f;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint2 lo = read_transposed(lv + 16 * c * Sh::kV + 64 * j),
-                                        hi = read_transposed(lv + (16 * c + 8) * Sh::kV + 64 * j);
-                            u32x4_t v = {lo.x, lo.y, hi.x, hi.y};
-                            if constexpr (decltype(care)::value)
-                                for (int e = 0; e < 4; ++e) v[e] = drop_not_finite(v[e]);
-                            x.o[j] = mfma_32x32x16(v, pk[c], x.o[j]);
-                        }
-                    }
-                };
-                if (scalar(sh.broken[buf]) != k0 + 1) {
-                    add(std::false_type{});
-                } else {
-                    add(std::true_type{});
-#pragma unroll 1
-                    for (int key = 0; key < kKeys; ++key)
-#pragma unroll
-                        for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                add_not_finite(reinterpret_cast<float *>(&x.o[j]) + 4 * i,
-                                               *reinterpret_cast<const uint2 *>(sh.v[buf] + key * Sh::kV + 64 * j +
-                                                                                16 * i + 8 * h),
-                                               k0 + key < seen);
-                }
+            if (k0 < wave_sees) {
+                uint64_t absent = 0;
+                for (int k = 0; k < kWaves; ++k) absent |= sh.absent[buf][k];
+                if (k0 + kKeys > wave_all_see || scalar64((int64_t)absent) != 0)
+                    round(k0, buf, std::true_type{});
+                else
+                    round(k0, buf, std::false_type{});
             }
-            if (k0 + kKeys < p.hi) store(k0 + kKeys, buf ^ 1);
-            __syncthreads();
+            if (more) store(buf ^ 1);
         }
         x.l += __shfl_xor(x.l, 32);
         if (!p.split) {
-            if (live) many_results<D>(a, w, x, row, qh, h);
+            if (live) {
+                const float f = result_factor(a, w.g, x.l);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        put_columns(a, row, qh, D, 32 * j + 8 * i + 4 * h, f,
+                                    f32x4_t{x.o[j][4 * i], x.o[j][4 * i + 1], x.o[j][4 * i + 2], x.o[j][4 * i + 3]});
+                if (h == 0) put_stats(a, row, qh, x.m, x.l);
+            }
         } else {
             if (any) {
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        put_pair(piece_sums<D>(a, p.slot, wave, 8 * j + i), x.o[j][2 * i], x.o[j][2 * i + 1]);
-                if (h == 0) put_pair(piece_stats<D>(a, p.slot, wave), x.m, x.l);
+                        *piece_sums<D>(a, p.slot, wave, 8 * j + i) = make_float2(x.o[j][2 * i], x.o[j][2 * i + 1]);
+                if (h == 0) *piece_stats<D>(a, p.slot, wave) = make_float2(x.m, x.l);
             }
-            if (last_of(a, p, &sh.last) && any) {
-                x.m = -INFINITY;
-                x.l = 0.0f;
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) x.o[j] = f32x16_t{};
-#pragma unroll 1
-                for (int k = 0; k < p.count; ++k) {  // in their order
-                    const int slot = piece_slot(w.r, p.first + k, w.at);
-                    const float2 ml = get_pair(piece_stats<D>(a, slot, wave));
-                    const float m2 = fmaxf(x.m, ml.x), base = base_of(m2);
-                    const float f = exp2_fast(x.m - base), f2 = exp2_fast(ml.x - base);
-                    x.m = m2;
-                    x.l = x.l * f + ml.y * f2;
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 o = get_pair(piece_sums<D>(a, slot, wave, 8 * j + i));
-                            x.o[j][2 * i] = x.o[j][2 * i] * f + o.x * f2;
-                            x.o[j][2 * i + 1] = x.o[j][2 * i + 1] * f + o.y * f2;
-                        }
-                }
-                if (live) many_results<D>(a, w, x, row, qh, h);
-            }
+            if (p.begins && threadIdx.x == 0)
+                a.joins[w.w] = {p.count, p.slot, t.row0 + t.first, t.count, w.g, {}};
         }
-        if (tid < 2) sh.broken[tid] = 0;
         __syncthreads();
     } while (w.next(a));
+}
+
+// The pieces of split tiles, in their order.  A wave takes 32 rows of a tile and
+// 16 columns of each; the tiles are those that the workgroups before noted.
+template <int D>
+__global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
+    constexpr int kPairs = 4, kItems = kWaves * (D / 4 / kPairs);  // of a lane; of a tile
+    __shared__ int tiles[kManyGroups], scratch[kWaves + 1];
+    const int lane = tl::lane_id(), h = lane / 32;
+    int total = 0;
+    for (int e0 = 0; e0 < a.groups_of_threads; e0 += kThreads) {
+        const int e = e0 + threadIdx.x;
+        const bool split = e < a.groups_of_threads && a.joins[e].pieces > 0;
+        int more;
+        const int at = tl::block_excl_scan<kThreads>(split, scratch, more);
+        if (split) tiles[total + at] = e;
+        total += more;
+    }
+    __syncthreads();
+    for (int item = blockIdx.x * kWaves + tl::wave_id(); item < total * kItems; item += gridDim.x * kWaves) {
+        const int first = tiles[item / kItems], quarter = item % kItems % kWaves, pair = item % kItems / kWaves * kPairs;
+        const Join t = a.joins[first];
+        const int r = quarter * 32 + lane % 32;
+        if (quarter * 32 >= t.rows) continue;
+        float m = -INFINITY, l = 0.0f;
+        float2 o[kPairs] = {};
+        constexpr int kAt = 4;
+        for (int k0 = 0; k0 < t.pieces; k0 += kAt) {
+            float2 ml[kAt], v[kAt][kPairs];
+#pragma unroll
+            for (int u = 0; u < kAt; ++u) {
+                const int k = min(k0 + u, t.pieces - 1), slot = k == 0 ? t.slot : 2 * (first + k);
+                ml[u] = *piece_stats<D>(a, slot, quarter);
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) v[u][i] = *piece_sums<D>(a, slot, quarter, pair + i);
+            }
+#pragma unroll
+            for (int u = 0; u < kAt; ++u) {
+                if (k0 + u >= t.pieces) break;
+                const float m2 = fmaxf(m, ml[u].x), base = base_of(m2);
+                const float f = exp2_fast(m - base), f2 = exp2_fast(ml[u].x - base);
+                m = m2;
+                l = l * f + ml[u].y * f2;
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i)
+                    o[i] = make_float2(o[i].x * f + v[u][i].x * f2, o[i].y * f + v[u][i].y * f2);
+            }
+        }
+        if (r >= t.rows) continue;
+        const int64_t row = t.row + r / a.each;
+        const int qh = t.g * a.each + r % a.each;
+        const float f = result_factor(a, t.g, l);
+#pragma unroll
+        for (int i = 0; i < kPairs; i += 2)
+            put_columns(a, row, qh, D, 32 * ((pair + i) / 8) + 8 * ((pair + i) % 8 / 2) + 4 * h, f,
+                        f32x4_t{o[i].x, o[i].y, o[i + 1].x, o[i + 1].y});
+        if (pair == 0 && h == 0) put_stats(a, row, qh, m, l);
+    }
 }
 
 template <int D>
@@ -343,6 +427,10 @@ hipError_t go(const AttendArgs &a, hipStream_t st) {
         attend_many_kernel<D, true><<<grid, block, 0, st>>>(a);
     else
         attend_many_kernel<D, false><<<grid, block, 0, st>>>(a);
+    if (hipError_t e = hipGetLastError()) return e;
+    // (no tile that the table allows is worth cutting)
+    if (kTileCost + (int64_t)a.table_cols * a.cache.page <= kManyWhole) return hipSuccess;
+    attend_join_kernel<D><<<dim3(kJoinGroups), block, 0, st>>>(a);
     return hipGetLastError();
 }
 

@@ -62,7 +62,7 @@ def append(L, **kw):
 CACHE_REFUSED = [dict(kc=0), dict(vc=0x80008), dict(ps=4100), dict(ts=120), dict(hs=64), dict(hs=132), dict(pages=0),
                  dict(page=0), dict(ks=0x100), dict(vs=0x100), dict(ks=0x102, vs=0x200), dict(ks=0x100, vs=0x200, hs=136),
                  dict(kv=0), dict(kv=3), dict(dim=0), dict(dim=120), dict(n=-1)]
-CACHE_UNSUPPORTED = [dict(pages=1 << 20, page=1 << 12), dict(ps=1 << 40), dict(n=(1 << 20) + 1),
+CACHE_UNSUPPORTED = [dict(pages=1 << 20, page=1 << 12), dict(ps=1 << 35), dict(n=(1 << 20) + 1),
                      dict(dim=272, ldq=4096, ldk=4096, ldv=4096, ldo=4096, hs=272, ts=1088, ps=1 << 20)]
 
 
