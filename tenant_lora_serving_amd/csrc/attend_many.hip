@@ -32,6 +32,9 @@ __device__ __forceinline__ f32x16_t mfma_32x32x16(const u32x4_t a, const u32x4_t
 }
 
 constexpr int kKeys = kManyStep;
+constexpr int kWaitLoads = 0x0f70;  // s_waitcnt vmcnt(0)
+// The larger of two, NaN if one is (v_maximum3_f32; fmaxf takes a step more for each).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 // Rows of keys lie side by side, 16-byte chunk c of key j at place c ^ k_turn(j)
 // or c ^ v_turn(j): 16 keys' reads of one chunk of K, and 4 keys' reads of 64
 // bytes of V, then fall on different banks.
@@ -39,8 +42,9 @@ template <int D>
 struct ManyShared {
     static constexpr int kRow = 2 * D;
     char k[2][kKeys * kRow], v[2][kKeys * kRow];
-    uint64_t absent[2][kWaves];  // keys whose page the cache does not have
+    uint64_t absent[2][kWaves];  // keys whose page the cache does not have (when careful)
     Found found;
+    int again;
     static __device__ __forceinline__ int k_turn(int key) { return key & (D == 64 ? 7 : 15); }
     static __device__ __forceinline__ int v_turn(int key) {
         return D == 64 ? (key & 2) << 1 : (key & 3) << 2 | (key & 4) >> 1;
@@ -142,199 +146,212 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
         // (a scale of 0, of a head that is all zeros, must not meet the masks' infinity)
         const float cf = fmaxf(a.scale * (F8 ? a.cache.k_scale[w.g] : 1.0f), 1e-30f);
         RowState<D> x;
-        x.m = -INFINITY;
-        x.l = 0.0f;
+        // The piece's keys.  The quick way leaves out two things that hardly ever
+        // happen, keys on pages that the cache does not have and, among the values of
+        // keys that some rows must not see, infinities and NaN, which p = 0 turns into
+        // NaN; it returns whether it met one, and then all is done again carefully.
+        auto attend = [&](auto careful) {
+            constexpr bool kCareful = decltype(careful)::value;
+            x.m = -INFINITY;
+            x.l = 0.0f;
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) x.o[j] = f32x16_t{};
-        if (a.state_in && p.begins && live) {
-            const int64_t rh = row * (a.kv * a.each) + qh;
-            const float2 ml = *reinterpret_cast<const float2 *>(a.state_in + 2 * rh);
-            x.m = ml.x;
-            x.l = h == 0 ? ml.y : 0.0f;  // (the sum is one over the two lanes of a row)
-            if (x.m != -INFINITY)
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x4_t o = *reinterpret_cast<const f32x4_t *>(a.sums_in + rh * D + 32 * j + 8 * i + 4 * h);
-                        for (int e = 0; e < 4; ++e) x.o[j][4 * i + e] = o[e];
-                    }
-        }
-
-        u32x4_t kr[F8 ? kLoads : 1], vr[F8 ? kLoads : 1];
-        int page[kLoads], in_page[kLoads];
-        auto pages = [&](int k0) {
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const int key = k0 + key_of(u), at = page_of(a.div, key);
-                in_page[u] = key - at * a.cache.page;
-                page[u] = key < p.hi ? table[at] : -1;
-            }
-        };
-        // Chunks of absent keys and past the head's columns are read from zeros:
-        // their scores are masked, but an infinity or NaN among their values
-        // would make NaN of p = 0.
-        auto start = [&](int k0, int buf) {
-            uint64_t absent = 0;
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const bool there = (uint32_t)page[u] < (uint32_t)a.cache.pages;
-                if (__any(!there)) {  // one bit a key, from the first of its lanes
-                    const uint64_t bits = __ballot(!there);
-                    for (int e = 0; e < kOfWave; ++e)
-                        absent |= ((bits >> (e * kLanes)) & 1) << ((u * kWaves + wave) * kOfWave + e);
-                }
-                const uint64_t off = token_offset(a, page[u], in_page[u]);
-                if constexpr (F8) {
-                    const bool read = there && lc < a.dim / 16;
-                    kr[u] = tl::ld16(read ? kh + off + lc * 16 : a.zeros);
-                    vr[u] = tl::ld16(read ? vh + off + lc * 16 : a.zeros);
-                } else {
-                    // (the place is the lane's, the chunk that belongs there comes from the turn)
-                    const int key = key_of(u), ck = lc ^ Sh::k_turn(key), cv = lc ^ Sh::v_turn(key);
-                    const int at = (u * kWaves + wave) * kWave * 16;
-                    load_lds(there && ck < a.dim / 8 ? kh + off + ck * 16 : a.zeros, lds_address(sh.k[buf]) + at);
-                    load_lds(there && cv < a.dim / 8 ? vh + off + cv * 16 : a.zeros, lds_address(sh.v[buf]) + at);
-                }
-            }
-            if (lane == 0) sh.absent[buf][wave] = absent;
-        };
-        auto store = [&](int buf) {
-            if constexpr (F8) {
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    const int key = key_of(u), tk = Sh::k_turn(key), tv = Sh::v_turn(key);
-                    char *const ks = sh.k[buf] + key * Sh::kRow, *const vs = sh.v[buf] + key * Sh::kRow;
-                    tl::st16(ks + ((2 * lc) ^ tk) * 16, widen8(kr[u].x, kr[u].y));
-                    tl::st16(ks + ((2 * lc + 1) ^ tk) * 16, widen8(kr[u].z, kr[u].w));
-                    tl::st16(vs + ((2 * lc) ^ tv) * 16, widen8(vr[u].x, vr[u].y));
-                    tl::st16(vs + ((2 * lc + 1) ^ tv) * 16, widen8(vr[u].z, vr[u].w));
-                }
-            }
-        };
-        auto round = [&](int k0, int buf, auto masked) {
-            f32x16_t s[2] = {};
-            const char *const lk = sh.k[buf] + lane % 32 * Sh::kRow;
-            const int tk = Sh::k_turn(lane % 32);  // (key 32 more has the same)
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    s[b] = mfma_32x32x16(tl::ld16(lk + 32 * b * Sh::kRow + ((2 * kk + h) ^ tk) * 16), q[kk], s[b]);
-            if constexpr (decltype(masked)::value) {
-                uint64_t absent = 0;
-                for (int k = 0; k < kWaves; ++k) absent |= sh.absent[buf][k];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int key = 32 * b + 8 * (i / 4) + 4 * h + i % 4;
-                        if (k0 + key >= seen || ((absent >> key) & 1)) s[b][i] = -INFINITY;
-                    }
-            }
-            float big = fmaxf(s[0][0], s[1][0]);
-#pragma unroll
-            for (int i = 1; i < 16; ++i) big = fmaxf(big, fmaxf(s[0][i], s[1][i]));
-            big = fmaxf(big, __shfl_xor(big, 32));
-            // The sums stay relative to an older maximum until a score passes it by
-            // 2^8: p may be that large as well, and scaling the sums costs as much
-            // as a quarter of a product.
-            const float m2 = fmaxf(x.m, big * cf);
-            if (__any(m2 > x.m + 8.0f)) {
-                const float f = exp2_fast(x.m - base_of(m2));
-                x.m = m2;
-                x.l *= f;
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) x.o[j] *= f;
-            }
-            const float base = base_of(x.m);
-            u32x4_t pk[4];
-            float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {  // 16 keys each
-                float pr[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) pr[i] = exp2_fast(fmaf(s[c / 2][8 * (c % 2) + i], cf, -base));
-                l0 += (pr[0] + pr[1]) + (pr[2] + pr[3]);
-                l1 += (pr[4] + pr[5]) + (pr[6] + pr[7]);
-                pk[c] = u32x4_t{tl::pack_bf16x2(pr[0], pr[1]), tl::pack_bf16x2(pr[2], pr[3]),
-                                tl::pack_bf16x2(pr[4], pr[5]), tl::pack_bf16x2(pr[6], pr[7])};
-            }
-            x.l += l0 + l1;
-            // keys 16 c + 4 h + lane % 16 / 4 and 8 more, columns 32 j + 16 (lane / 16 % 2) + 4 (lane % 4) .. of V
-            const int vkey = 4 * h + lane % 16 / 4;
-            const char *const lv = sh.v[buf] + vkey * Sh::kRow + lane % 2 * 8;
-            const int tv = Sh::v_turn(vkey), vchunk = lane / 16 % 2 * 2 + lane % 4 / 2;
-            auto values = [&](int c, int j) {  // (key 8 more has the same turn)
-                const char *const at = lv + 16 * c * Sh::kRow + ((4 * j + vchunk) ^ tv) * 16;
-                const uint2 lo = read_transposed(at), hi = read_transposed(at + 8 * Sh::kRow);
-                return u32x4_t{lo.x, lo.y, hi.x, hi.y};
-            };
-            bool broken = false;
-            if constexpr (decltype(masked)::value) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) broken |= not_finite(values(c, j));
-                broken = __any(broken);
-                asm volatile("" ::: "memory");  // (read again below, not kept in registers)
-            }
-            if (!broken) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) x.o[j] = mfma_32x32x16(values(c, j), pk[c], x.o[j]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j) {
-                        u32x4_t v = values(c, j);
-                        for (int e = 0; e < 4; ++e) v[e] = drop_not_finite(v[e]);
-                        x.o[j] = mfma_32x32x16(v, pk[c], x.o[j]);
-                    }
-#pragma unroll 1
-                for (int key = 0; key < kKeys; ++key) {
-                    const char *const at = sh.v[buf] + key * Sh::kRow + 8 * h;
+            for (int j = 0; j < D / 32; ++j) x.o[j] = f32x16_t{};
+            if (a.state_in && p.begins && live) {
+                const int64_t rh = row * (a.kv * a.each) + qh;
+                const float2 ml = *reinterpret_cast<const float2 *>(a.state_in + 2 * rh);
+                x.m = ml.x;
+                x.l = h == 0 ? ml.y : 0.0f;  // (the sum is one over the two lanes of a row)
+                if (x.m != -INFINITY)
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(at + ((4 * j + i) ^ Sh::v_turn(key)) * 16);
-                            float f[4] = {};
-                            add_not_finite(f, v, k0 + key < seen);
-                            for (int e = 0; e < 4; ++e) x.o[j][4 * i + e] += f[e];
+                            const f32x4_t o =
+                                *reinterpret_cast<const f32x4_t *>(a.sums_in + rh * D + 32 * j + 8 * i + 4 * h);
+                            for (int e = 0; e < 4; ++e) x.o[j][4 * i + e] = o[e];
+                        }
+            }
+            bool met = false;
+            u32x4_t kr[F8 ? kLoads : 1], vr[F8 ? kLoads : 1];
+            int page[kLoads], in_page[kLoads];
+            auto pages = [&](int k0) {
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int key = k0 + key_of(u), at = page_of(a.div, key);
+                    in_page[u] = key - at * a.cache.page;
+                    page[u] = key < p.hi ? table[at] : -1;
+                }
+            };
+            // Chunks of absent keys and past the head's columns are read from zeros:
+            // their scores are masked, but an infinity or NaN among their values
+            // would make NaN of p = 0.
+            auto start = [&](int k0, int buf) {
+                uint64_t absent = 0;
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const bool there = (uint32_t)page[u] < (uint32_t)a.cache.pages;
+                    if constexpr (kCareful) {  // one bit a key, from the first of its lanes
+                        const uint64_t bits = __ballot(!there);
+                        for (int e = 0; e < kOfWave; ++e)
+                            absent |= ((bits >> (e * kLanes)) & 1) << ((u * kWaves + wave) * kOfWave + e);
+                    } else {
+                        met |= !there && k0 + key_of(u) < p.hi;
+                    }
+                    const uint64_t off = token_offset(a, page[u], in_page[u]);
+                    if constexpr (F8) {
+                        const bool read = there && lc < a.dim / 16;
+                        kr[u] = tl::ld16(read ? kh + off + lc * 16 : a.zeros);
+                        vr[u] = tl::ld16(read ? vh + off + lc * 16 : a.zeros);
+                    } else {
+                        // (the place is the lane's, the chunk that belongs there comes from the turn)
+                        const int key = key_of(u), ck = lc ^ Sh::k_turn(key), cv = lc ^ Sh::v_turn(key);
+                        const int at = (u * kWaves + wave) * kWave * 16;
+                        load_lds(there && ck < a.dim / 8 ? kh + off + ck * 16 : a.zeros, lds_address(sh.k[buf]) + at);
+                        load_lds(there && cv < a.dim / 8 ? vh + off + cv * 16 : a.zeros, lds_address(sh.v[buf]) + at);
+                    }
+                }
+                if (kCareful && lane == 0) sh.absent[buf][wave] = absent;
+            };
+            auto store = [&](int buf) {
+                if constexpr (F8) {
+#pragma unroll
+                    for (int u = 0; u < kLoads; ++u) {
+                        const int key = key_of(u), tk = Sh::k_turn(key), tv = Sh::v_turn(key);
+                        char *const ks = sh.k[buf] + key * Sh::kRow, *const vs = sh.v[buf] + key * Sh::kRow;
+                        tl::st16(ks + ((2 * lc) ^ tk) * 16, widen8(kr[u].x, kr[u].y));
+                        tl::st16(ks + ((2 * lc + 1) ^ tk) * 16, widen8(kr[u].z, kr[u].w));
+                        tl::st16(vs + ((2 * lc) ^ tv) * 16, widen8(vr[u].x, vr[u].y));
+                        tl::st16(vs + ((2 * lc + 1) ^ tv) * 16, widen8(vr[u].z, vr[u].w));
+                    }
+                }
+            };
+            // scores of the lane's row: key 32 b + 8 (i / 4) + 4 h + i % 4
+            const char *const lk = sh.k[0] + lane % 32 * Sh::kRow;
+            const int tk = Sh::k_turn(lane % 32);  // (key 32 more has the same)
+            // keys 16 c + 4 h + lane % 16 / 4 and 8 more, columns 32 j + 16 (lane / 16 % 2) + 4 (lane % 4) .. of V
+            const int vkey = 4 * h + lane % 16 / 4;
+            const char *const lv = sh.v[0] + vkey * Sh::kRow + lane % 2 * 8;
+            const int tv = Sh::v_turn(vkey), vchunk = lane / 16 % 2 * 2 + lane % 4 / 2;
+            auto round = [&](int k0, int buf) {
+                f32x16_t s[2] = {};
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        s[b] = mfma_32x32x16(tl::ld16(lk + buf * (kKeys * Sh::kRow) + 32 * b * Sh::kRow +
+                                                      ((2 * kk + h) ^ tk) * 16), q[kk], s[b]);
+                if (kCareful || k0 + kKeys > wave_all_see) {
+                    uint64_t absent = 0;
+                    if constexpr (kCareful)
+                        for (int k = 0; k < kWaves; ++k) absent |= sh.absent[buf][k];
+                    const int left = seen - k0 - 4 * h;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int key = 32 * b + 8 * (i / 4) + i % 4;
+                            if (key >= left || (kCareful && ((absent >> (key + 4 * h)) & 1))) s[b][i] = -INFINITY;
                         }
                 }
-            }
-        };
-        if (p.lo < p.hi) {
-            pages(p.lo);
-            start(p.lo, 0);
-            pages(p.lo + kKeys);
-            store(0);
-        }
-        int buf = 0;
+                float big = larger(s[0][0], s[1][0]);
+#pragma unroll
+                for (int i = 1; i < 16; ++i) big = larger(big, larger(s[0][i], s[1][i]));
+                big = larger(big, __shfl_xor(big, 32));
+                // The sums stay relative to an older maximum until a score passes it by
+                // 2^8: p may be that large as well, and scaling the sums costs as much
+                // as a quarter of a product.
+                const float m2 = fmaxf(x.m, big * cf);
+                if (__any(m2 > x.m + 8.0f)) {
+                    const float f = exp2_fast(x.m - base_of(m2));
+                    x.m = m2;
+                    x.l *= f;
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) x.o[j] *= f;
+                }
+                const float base = base_of(x.m);
+                u32x4_t pk[4];
+                float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {  // 16 keys each
+                    float pr[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) pr[i] = exp2_fast(fmaf(s[c / 2][8 * (c % 2) + i], cf, -base));
+                    l0 += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+                    l1 += (pr[4] + pr[5]) + (pr[6] + pr[7]);
+                    pk[c] = u32x4_t{tl::pack_bf16x2(pr[0], pr[1]), tl::pack_bf16x2(pr[2], pr[3]),
+                                    tl::pack_bf16x2(pr[4], pr[5]), tl::pack_bf16x2(pr[6], pr[7])};
+                }
+                x.l += l0 + l1;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) {  // (key 8 more has the same turn)
+                        const char *const at =
+                            lv + buf * (kKeys * Sh::kRow) + 16 * c * Sh::kRow + ((4 * j + vchunk) ^ tv) * 16;
+                        const uint2 lo = read_transposed(at), hi = read_transposed(at + 8 * Sh::kRow);
+                        u32x4_t v = {lo.x, lo.y, hi.x, hi.y};
+                        if constexpr (kCareful)
+                            for (int e = 0; e < 4; ++e) v[e] = drop_not_finite(v[e]);
+                        x.o[j] = mfma_32x32x16(v, pk[c], x.o[j]);
+                    }
+                if constexpr (kCareful) {
 #pragma unroll 1
-        for (int k0 = p.lo; k0 < p.hi; k0 += kKeys, buf ^= 1) {
-            if constexpr (!F8) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                    for (int key = 0; key < kKeys; ++key) {
+                        const char *const at = sh.v[buf] + key * Sh::kRow + 8 * h;
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint2 v =
+                                    *reinterpret_cast<const uint2 *>(at + ((4 * j + i) ^ Sh::v_turn(key)) * 16);
+                                float f[4] = {};
+                                add_not_finite(f, v, k0 + key < seen);
+                                for (int e = 0; e < 4; ++e) x.o[j][4 * i + e] += f[e];
+                            }
+                    }
+                }
+            };
+            if (p.lo < p.hi) {
+                pages(p.lo);
+                start(p.lo, 0);
+                pages(p.lo + kKeys);
+                store(0);
+            }
+            int buf = 0;
+#pragma unroll 1
+            for (int k0 = p.lo; k0 < p.hi; k0 += kKeys, buf ^= 1) {
+                // (the builtin, since the compiler counts what it waits for: it would
+                // otherwise wait for the rows of q in here, and so for the next keys)
+                __builtin_amdgcn_s_waitcnt(kWaitLoads);
+                __syncthreads();
+                const bool more = k0 + kKeys < p.hi;
+                if (more) {
+                    start(k0 + kKeys, buf ^ 1);
+                    pages(k0 + 2 * kKeys);
+                }
+                if (k0 < wave_sees) round(k0, buf);
+                if (more) store(buf ^ 1);
+            }
+            x.l += __shfl_xor(x.l, 32);
+            if constexpr (kCareful) return false;
+            if (live) {
+                float size = 0.0f;
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) size = larger(size, fabsf(x.o[j][i]));
+                met |= !(size < INFINITY);
+            }
+            return met;
+        };
+        if (threadIdx.x == 0) sh.again = 0;
+        __syncthreads();
+        if (__any(attend(std::false_type{})) && lane == 0) sh.again = 1;
+        __syncthreads();
+        if (scalar(sh.again)) {
+            attend(std::true_type{});
             __syncthreads();
-            const bool more = k0 + kKeys < p.hi;
-            if (more) {
-                start(k0 + kKeys, buf ^ 1);
-                pages(k0 + 2 * kKeys);
-            }
-            if (k0 < wave_sees) {
-                uint64_t absent = 0;
-                for (int k = 0; k < kWaves; ++k) absent |= sh.absent[buf][k];
-                if (k0 + kKeys > wave_all_see || scalar64((int64_t)absent) != 0)
-                    round(k0, buf, std::true_type{});
-                else
-                    round(k0, buf, std::false_type{});
-            }
-            if (more) store(buf ^ 1);
         }
-        x.l += __shfl_xor(x.l, 32);
         if (!p.split) {
             if (live) {
                 const float f = result_factor(a, w.g, x.l);
