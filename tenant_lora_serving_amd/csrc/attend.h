@@ -117,18 +117,21 @@ struct Found {
     int job;
 };
 
-// A workgroup's walk through the tiles of its range.
+// A workgroup's walk through the tiles of its range.  (All of it is the same in
+// every lane; divisions are computed by the vector unit, and what follows from
+// them stays there, in registers that the kernels are short of, unless it is
+// taken back to scalar ones.)
 struct Walk {
     Ranges r;
     int64_t total, at, end;  // cost at which the tile begins; at which the range ends
     int w, tokens;
-    int j, g, i;
+    int j, g, i, tiles;
     Job job;
 
     // By every thread of the workgroup; false if nothing is left for it.
     __device__ __forceinline__ bool find(const AttendArgs &a, int rows, int least, int whole, Found &found) {
         const int tid = threadIdx.x, lane = tl::lane_id();
-        tokens = rows / a.each;
+        tokens = scalar(rows / a.each);
         w = workgroup_of(a);
         const int per = (a.jobs + kThreads - 1) / kThreads, j0 = min(tid * per, a.jobs), j1 = min(j0 + per, a.jobs);
         int64_t mine = 0;
@@ -147,6 +150,7 @@ struct Walk {
         }
         total = scalar64(total);
         r = ranges_of(total, a.groups_of_threads, least, whole);
+        r = {scalar64(r.size), scalar64(r.whole)};
         const int64_t begin = w * r.size;
         end = begin + r.size < total ? begin + r.size : total;
         if (begin >= total) return false;
@@ -164,22 +168,30 @@ struct Walk {
         __syncthreads();
         j = scalar(found.job);
         load(a);
-        const int64_t base = scalar64(found.base), head = job_cost(a, job.s, tokens);
-        g = (int)((begin - base) / head);
-        i = tile_at(job.s, tokens, a.causal, begin - base - g * head);
-        at = base + g * head + tiles_cost(job.s, tokens, a.causal, i);
+        const int64_t base = scalar64(found.base), head = scalar64(job_cost(a, job.s, tokens));
+        g = scalar((int)((begin - base) / head));
+        i = scalar(tile_at(job.s, tokens, a.causal, begin - base - g * head));
+        at = scalar64(base + g * head + tiles_cost(job.s, tokens, a.causal, i));
         return true;
     }
     __device__ __forceinline__ void load(const AttendArgs &a) {
         const Job b = job_of(a, j);
         job = {{scalar(b.s.rows), scalar(b.s.len)}, scalar(b.row0)};
+        tiles = scalar(tiles_of(job.s.rows, tokens));
     }
-    __device__ __forceinline__ int keys(const AttendArgs &a) const { return tile_keys(job.s, tokens, a.causal, i); }
+    __device__ __forceinline__ int keys(const AttendArgs &a) const {
+        return scalar(tile_keys(job.s, tokens, a.causal, i));
+    }
+    __device__ __forceinline__ Piece piece(int keys, int step) const {
+        const Piece p = piece_of(r, w, at, keys, step);
+        return {scalar(p.mine) != 0, scalar(p.split) != 0, scalar(p.begins) != 0, scalar(p.lo), scalar(p.hi),
+                scalar(p.first), scalar(p.count), scalar(p.slot)};
+    }
     // The next tile; false behind the range's last one.
     __device__ __forceinline__ bool next(const AttendArgs &a) {
         at += kTileCost + keys(a);
         if (at >= end) return false;
-        if (++i < tiles_of(job.s.rows, tokens)) return true;
+        if (++i < tiles) return true;
         i = 0;
         if (++g < a.kv) return true;
         g = 0;

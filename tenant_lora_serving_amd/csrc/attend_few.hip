@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_few_kernel(A
     const char *const kc = static_cast<const char *>(a.cache.k), *const vc = static_cast<const char *>(a.cache.v);
     do {
         const int keys = w.keys(a);
-        const Piece p = piece_of(w.r, w.w, w.at, keys, kFewStep);
+        const Piece p = w.piece(keys, kFewStep);
         if (!p.mine) continue;
         const TileRows t(a, w);
         const int32_t *const table = table_of(a, w.j);

@@ -31,10 +31,15 @@ __device__ __forceinline__ f32x16_t mfma_32x32x16(const u32x4_t a, const u32x4_t
                                                    __builtin_bit_cast(tl::bf16x8_t, b), c, 0, 0, 0);
 }
 
-constexpr int kKeys = kManyStep;
+constexpr int kKeys = kManyStep, kHalf = kKeys / 2;
 constexpr int kWaitLoads = 0x0f70;  // s_waitcnt vmcnt(0)
 // The larger of two, NaN if one is (v_maximum3_f32; fmaxf takes a step more for each).
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+// The larger of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ float larger_of_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return larger(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 // Rows of keys lie side by side, 16-byte chunk c of key j at place c ^ k_turn(j)
 // or c ^ v_turn(j): 16 keys' reads of one chunk of K, and 4 keys' reads of 64
 // bytes of V, then fall on different banks.
@@ -58,6 +63,13 @@ struct ManyShared {
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds(const char *p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p) : "m0", "memory");
+}
+// The same from `base` (of the wave) + `off` (of the lane).
+__device__ __forceinline__ void load_lds(const char *base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds), "v"(off), "s"(base)
+                 : "m0", "memory");
 }
 #pragma clang diagnostic pop
 __device__ __forceinline__ uint32_t lds_address(const char *p) {
@@ -104,11 +116,15 @@ __device__ __forceinline__ float2 *piece_stats(const AttendArgs &a, int slot, in
            tl::lane_id() % 32;
 }
 
+// Even: pages hold whole groups of the keys that a load instruction takes, so
+// that places are worked out once a wave, with scalar instructions.
 template <int D, bool F8>
+constexpr int kKeysOfLoad = kWave * 16 / (D * (F8 ? 1 : 2));
+template <int D, bool F8, bool Even>
 __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(AttendArgs a) {
     using Sh = ManyShared<D>;
     constexpr int kSize = F8 ? 1 : 2;
-    constexpr int kLanes = D * kSize / 16, kOfWave = kWave / kLanes;  // lanes of a key; keys of a wave's load
+    constexpr int kLanes = D * kSize / 16, kOfWave = kKeysOfLoad<D, F8>;  // lanes of a key; keys of a wave's load
     constexpr int kLoads = kKeys / (kWaves * kOfWave);
     __shared__ Sh sh;
     Walk w;
@@ -118,10 +134,11 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
     // this lane's key of load u is (u * kWaves + wave) * kOfWave + lr
     const int lc = lane % kLanes, lr = lane / kLanes;
     auto key_of = [&](int u) { return (u * kWaves + wave) * kOfWave + lr; };
+    const uint32_t from = lr * a.token_units * 16;  // (used where the keys of a load are on one page)
     const char *const kc = static_cast<const char *>(a.cache.k), *const vc = static_cast<const char *>(a.cache.v);
     do {
         const int keys = w.keys(a);
-        const Piece p = piece_of(w.r, w.w, w.at, keys, kManyStep);
+        const Piece p = w.piece(keys, kManyStep);
         if (!p.mine) continue;
         const TileRows t(a, w);
         const int32_t *const table = table_of(a, w.j);
@@ -134,9 +151,9 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
         const int64_t row = t.row0 + token;
         const int qh = w.g * a.each + (live ? r % a.each : 0);
         const int seen = live ? TileRows::seen(a, w.job.s, token) : 0;
-        // the keys that some of the wave's rows see, and that all do
-        const int wave_sees = any ? TileRows::seen(a, w.job.s, t.first + r_last / a.each) : 0;
-        const int wave_all_see = TileRows::seen(a, w.job.s, t.first + r_first / a.each);
+        // the keys that some of the wave's rows see, and that all rows of the tile do
+        const int wave_sees = scalar(any ? TileRows::seen(a, w.job.s, t.first + r_last / a.each) : 0);
+        const int tile_all_see = scalar(TileRows::seen(a, w.job.s, t.first));
         u32x4_t q[D / 16];
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -151,7 +168,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
         // keys that some rows must not see, infinities and NaN, which p = 0 turns into
         // NaN; it returns whether it met one, and then all is done again carefully.
         auto attend = [&](auto careful) {
-            constexpr bool kCareful = decltype(careful)::value;
+            constexpr bool kCareful = decltype(careful)::value, kQuick = Even && !kCareful;
             x.m = -INFINITY;
             x.l = 0.0f;
 #pragma unroll
@@ -173,93 +190,121 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
             }
             bool met = false;
             u32x4_t kr[F8 ? kLoads : 1], vr[F8 ? kLoads : 1];
-            int page[kLoads], in_page[kLoads];
-            auto pages = [&](int k0) {
+            // Pages of 64 keys' tokens, looked up a round ahead.  K is taken 32 keys
+            // before V, from k0 - 32.
+            int k_page[kLoads], v_page[kLoads];
+            auto key_in = [&](int k0, int u) { return k0 + (kQuick ? (u * kWaves + wave) * kOfWave : key_of(u)); };
+            auto pages = [&](int k0, int (&page)[kLoads]) {
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
-                    const int key = k0 + key_of(u), at = page_of(a.div, key);
-                    in_page[u] = key - at * a.cache.page;
-                    page[u] = key < p.hi ? table[at] : -1;
+                    const int key = key_in(k0, u);
+                    page[u] = key >= p.lo && key < p.hi ? table[page_of(a.div, key)] : kQuick ? 0 : -1;
                 }
             };
-            // Chunks of absent keys and past the head's columns are read from zeros:
-            // their scores are masked, but an infinity or NaN among their values
-            // would make NaN of p = 0.
-            auto start = [&](int k0, int buf) {
-                uint64_t absent = 0;
+            // One of K and V, 64 keys.  Chunks of absent keys and past the head's columns
+            // are read from zeros: their scores are masked, but an infinity or NaN among
+            // their values would make NaN of p = 0.
+            auto start = [&](int k0, const int (&page)[kLoads], const char *base, char *buf, auto turn, u32x4_t *regs) {
+                const uint32_t lds = lds_address(buf) + wave * kWave * 16;
+                const bool whole = !F8 && kQuick && a.dim == D && k0 >= p.lo && k0 + kKeys <= p.hi;
+                const char *from_u[kLoads];
+                bool known[kLoads];
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
-                    const bool there = (uint32_t)page[u] < (uint32_t)a.cache.pages;
-                    if constexpr (kCareful) {  // one bit a key, from the first of its lanes
-                        const uint64_t bits = __ballot(!there);
-                        for (int e = 0; e < kOfWave; ++e)
-                            absent |= ((bits >> (e * kLanes)) & 1) << ((u * kWaves + wave) * kOfWave + e);
+                    const int page_u = kQuick ? scalar(page[u]) : page[u], key = key_in(k0, u);
+                    const int in_page = key - page_of(a.div, key) * a.cache.page;
+                    known[u] = (uint32_t)page_u < (uint32_t)a.cache.pages;
+                    if constexpr (kQuick) {
+                        met |= !known[u];
+                        from_u[u] = base + token_offset(a, known[u] ? page_u : 0, key >= p.lo ? in_page : 0);
                     } else {
-                        met |= !there && k0 + key_of(u) < p.hi;
-                    }
-                    const uint64_t off = token_offset(a, page[u], in_page[u]);
-                    if constexpr (F8) {
-                        const bool read = there && lc < a.dim / 16;
-                        kr[u] = tl::ld16(read ? kh + off + lc * 16 : a.zeros);
-                        vr[u] = tl::ld16(read ? vh + off + lc * 16 : a.zeros);
-                    } else {
-                        // (the place is the lane's, the chunk that belongs there comes from the turn)
-                        const int key = key_of(u), ck = lc ^ Sh::k_turn(key), cv = lc ^ Sh::v_turn(key);
-                        const int at = (u * kWaves + wave) * kWave * 16;
-                        load_lds(there && ck < a.dim / 8 ? kh + off + ck * 16 : a.zeros, lds_address(sh.k[buf]) + at);
-                        load_lds(there && cv < a.dim / 8 ? vh + off + cv * 16 : a.zeros, lds_address(sh.v[buf]) + at);
+                        met |= !known[u] && key >= p.lo && key < p.hi;
+                        from_u[u] = base + token_offset(a, page_u, in_page);
                     }
                 }
-                if (kCareful && lane == 0) sh.absent[buf][wave] = absent;
+                if (whole) {
+#pragma unroll
+                    for (int u = 0; u < kLoads; ++u)
+                        load_lds(reinterpret_cast<const char *>(scalar64(reinterpret_cast<int64_t>(from_u[u]))),
+                                 from + (lc ^ turn(key_of(u))) * 16, lds + u * kThreads * 16);
+                    return;
+                }
+                // (places worked out here, not kept in registers through the rounds that do without)
+                int l = lane;
+                asm volatile("" : "+v"(l));
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int key = (u * kWaves + wave) * kOfWave + l / kLanes;
+                    const int chunk = F8 ? l % kLanes : l % kLanes ^ turn(key);
+                    const bool there =
+                        k0 + key >= p.lo && k0 + key < p.hi && known[u] && chunk < a.dim * kSize / 16;
+                    const uint32_t in_load = kQuick ? l / kLanes * a.token_units * 16 : 0;
+                    const char *const at_u = there ? from_u[u] + in_load + chunk * 16 : a.zeros;
+                    if constexpr (F8)
+                        regs[u] = tl::ld16(at_u);
+                    else
+                        load_lds(at_u, lds + u * kThreads * 16);
+                }
             };
-            auto store = [&](int buf) {
-                if constexpr (F8) {
+            auto store = [&](char *buf, auto turn, const u32x4_t *regs) {
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) {
+                    const int key = key_of(u), by = turn(key);
+                    char *const to = buf + key * Sh::kRow;
+                    tl::st16(to + ((2 * lc) ^ by) * 16, widen8(regs[u].x, regs[u].y));
+                    tl::st16(to + ((2 * lc + 1) ^ by) * 16, widen8(regs[u].z, regs[u].w));
+                }
+            };
+            auto k_turn = [](int key) { return Sh::k_turn(key); };
+            auto v_turn = [](int key) { return Sh::v_turn(key); };
+            auto start_k = [&](int k0, int buf) {
+                if (k0 - kHalf >= p.hi) return;
+                start(k0 - kHalf, k_page, kh, sh.k[buf], k_turn, kr);
+                if constexpr (kCareful) {  // one bit a key, from the first of its lanes
+                    uint64_t absent = 0;
 #pragma unroll
                     for (int u = 0; u < kLoads; ++u) {
-                        const int key = key_of(u), tk = Sh::k_turn(key), tv = Sh::v_turn(key);
-                        char *const ks = sh.k[buf] + key * Sh::kRow, *const vs = sh.v[buf] + key * Sh::kRow;
-                        tl::st16(ks + ((2 * lc) ^ tk) * 16, widen8(kr[u].x, kr[u].y));
-                        tl::st16(ks + ((2 * lc + 1) ^ tk) * 16, widen8(kr[u].z, kr[u].w));
-                        tl::st16(vs + ((2 * lc) ^ tv) * 16, widen8(vr[u].x, vr[u].y));
-                        tl::st16(vs + ((2 * lc + 1) ^ tv) * 16, widen8(vr[u].z, vr[u].w));
+                        const uint64_t bits = __ballot((uint32_t)k_page[u] >= (uint32_t)a.cache.pages);
+                        for (int e = 0; e < kOfWave; ++e)
+                            absent |= ((bits >> (e * kLanes)) & 1) << ((u * kWaves + wave) * kOfWave + e);
                     }
+                    if (lane == 0) sh.absent[buf][wave] = absent;
                 }
+                pages(k0 + kHalf, k_page);
             };
-            // scores of the lane's row: key 32 b + 8 (i / 4) + 4 h + i % 4
+            auto start_v = [&](int k0, int buf) {
+                if (k0 >= p.hi) return;
+                start(k0, v_page, vh, sh.v[buf], v_turn, vr);
+                pages(k0 + kKeys, v_page);
+            };
+            auto store_k = [&](int k0, int buf) {
+                if (F8 && k0 - kHalf < p.hi) store(sh.k[buf], k_turn, kr);
+            };
+            auto store_v = [&](int k0, int buf) {
+                if (F8 && k0 < p.hi) store(sh.v[buf], v_turn, vr);
+            };
+            // Scores of the lane's row with 32 keys: 8 (i / 4) + 4 h + i % 4 in register i.
+            // b: which half of the buffer.
             const char *const lk = sh.k[0] + lane % 32 * Sh::kRow;
             const int tk = Sh::k_turn(lane % 32);  // (key 32 more has the same)
-            // keys 16 c + 4 h + lane % 16 / 4 and 8 more, columns 32 j + 16 (lane / 16 % 2) + 4 (lane % 4) .. of V
-            const int vkey = 4 * h + lane % 16 / 4;
-            const char *const lv = sh.v[0] + vkey * Sh::kRow + lane % 2 * 8;
-            const int tv = Sh::v_turn(vkey), vchunk = lane / 16 % 2 * 2 + lane % 4 / 2;
-            auto round = [&](int k0, int buf) {
-                f32x16_t s[2] = {};
+            auto scores = [&](int buf, int b) {
+                f32x16_t s = {};
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
+                    s = mfma_32x32x16(tl::ld16(lk + (buf * kKeys + kHalf * b) * Sh::kRow + ((2 * kk + h) ^ tk) * 16), q[kk], s);
+                return s;
+            };
+            auto largest = [&](const f32x16_t &s) {
+                float big = s[0];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        s[b] = mfma_32x32x16(tl::ld16(lk + buf * (kKeys * Sh::kRow) + 32 * b * Sh::kRow +
-                                                      ((2 * kk + h) ^ tk) * 16), q[kk], s[b]);
-                if (kCareful || k0 + kKeys > wave_all_see) {
-                    uint64_t absent = 0;
-                    if constexpr (kCareful)
-                        for (int k = 0; k < kWaves; ++k) absent |= sh.absent[buf][k];
-                    const int left = seen - k0 - 4 * h;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int key = 32 * b + 8 * (i / 4) + i % 4;
-                            if (key >= left || (kCareful && ((absent >> (key + 4 * h)) & 1))) s[b][i] = -INFINITY;
-                        }
-                }
-                float big = larger(s[0][0], s[1][0]);
-#pragma unroll
-                for (int i = 1; i < 16; ++i) big = larger(big, larger(s[0][i], s[1][i]));
-                big = larger(big, __shfl_xor(big, 32));
-                // The sums stay relative to an older maximum until a score passes it by
-                // 2^8: p may be that large as well, and scaling the sums costs as much
-                // as a quarter of a product.
+                for (int i = 1; i < 16; ++i) big = larger(big, s[i]);
+                return big;  // (of the lane's half of the keys)
+            };
+            // The sums stay relative to an older maximum until a score passes it by
+            // 2^8: p may be that large as well, and scaling the sums costs as much
+            // as a quarter of a product.
+            auto rescale = [&](float big) {
+                big = larger_of_halves(big);
                 const float m2 = fmaxf(x.m, big * cf);
                 if (__any(m2 > x.m + 8.0f)) {
                     const float f = exp2_fast(x.m - base_of(m2));
@@ -268,69 +313,202 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j) x.o[j] *= f;
                 }
+            };
+            // o += p V for 32 keys, the first or second half of the buffer.  V: keys 16 c +
+            // 4 h + lane % 16 / 4 and 8 more, columns 32 j + 16 (lane / 16 % 2) + 4 (lane % 4) ..
+            const int vkey = 4 * h + lane % 16 / 4;
+            const char *const lv = sh.v[0] + vkey * Sh::kRow + lane % 2 * 8;
+            const int tv = Sh::v_turn(vkey), vchunk = lane / 16 % 2 * 2 + lane % 4 / 2;
+            auto add = [&](const f32x16_t &s, int buf, int b) {
                 const float base = base_of(x.m);
-                u32x4_t pk[4];
-                float l0 = 0.0f, l1 = 0.0f;
+                float l[2];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {  // 16 keys each
+                for (int c = 0; c < 2; ++c) {  // 16 keys each
                     float pr[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) pr[i] = exp2_fast(fmaf(s[c / 2][8 * (c % 2) + i], cf, -base));
-                    l0 += (pr[0] + pr[1]) + (pr[2] + pr[3]);
-                    l1 += (pr[4] + pr[5]) + (pr[6] + pr[7]);
-                    pk[c] = u32x4_t{tl::pack_bf16x2(pr[0], pr[1]), tl::pack_bf16x2(pr[2], pr[3]),
-                                    tl::pack_bf16x2(pr[4], pr[5]), tl::pack_bf16x2(pr[6], pr[7])};
-                }
-                x.l += l0 + l1;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int i = 0; i < 8; ++i) pr[i] = exp2_fast(fmaf(s[8 * c + i], cf, -base));
+                    l[c] = ((pr[0] + pr[1]) + (pr[2] + pr[3])) + ((pr[4] + pr[5]) + (pr[6] + pr[7]));
+                    const u32x4_t pk = {tl::pack_bf16x2(pr[0], pr[1]), tl::pack_bf16x2(pr[2], pr[3]),
+                                        tl::pack_bf16x2(pr[4], pr[5]), tl::pack_bf16x2(pr[6], pr[7])};
 #pragma unroll
                     for (int j = 0; j < D / 32; ++j) {  // (key 8 more has the same turn)
                         const char *const at =
-                            lv + buf * (kKeys * Sh::kRow) + 16 * c * Sh::kRow + ((4 * j + vchunk) ^ tv) * 16;
+                            lv + (buf * kKeys + kHalf * b + 16 * c) * Sh::kRow + ((4 * j + vchunk) ^ tv) * 16;
                         const uint2 lo = read_transposed(at), hi = read_transposed(at + 8 * Sh::kRow);
                         u32x4_t v = {lo.x, lo.y, hi.x, hi.y};
                         if constexpr (kCareful)
                             for (int e = 0; e < 4; ++e) v[e] = drop_not_finite(v[e]);
-                        x.o[j] = mfma_32x32x16(v, pk[c], x.o[j]);
-                    }
-                if constexpr (kCareful) {
-#pragma unroll 1
-                    for (int key = 0; key < kKeys; ++key) {
-                        const char *const at = sh.v[buf] + key * Sh::kRow + 8 * h;
-#pragma unroll
-                        for (int j = 0; j < D / 32; ++j)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint2 v =
-                                    *reinterpret_cast<const uint2 *>(at + ((4 * j + i) ^ Sh::v_turn(key)) * 16);
-                                float f[4] = {};
-                                add_not_finite(f, v, k0 + key < seen);
-                                for (int e = 0; e < 4; ++e) x.o[j][4 * i + e] += f[e];
-                            }
+                        x.o[j] = mfma_32x32x16(v, pk, x.o[j]);
                     }
                 }
+                x.l += l[0] + l[1];
             };
-            if (p.lo < p.hi) {
-                pages(p.lo);
-                start(p.lo, 0);
-                pages(p.lo + kKeys);
-                store(0);
-            }
-            int buf = 0;
-#pragma unroll 1
-            for (int k0 = p.lo; k0 < p.hi; k0 += kKeys, buf ^= 1) {
-                // (the builtin, since the compiler counts what it waits for: it would
-                // otherwise wait for the rows of q in here, and so for the next keys)
+            // add(s, buf, b) and, beside it, the next scores and the largest of them: each
+            // product has exponentials or maxima to run beside, and fragments that were
+            // read some products before.  (Left to the compiler, each fragment is read
+            // right before its product and waited for, and products, exponentials and
+            // products follow one another: MIXNOTE.)
+            auto mixed = [&](const f32x16_t &s, int buf, int b, f32x16_t &next, int next_buf, int next_b) {
+                constexpr int kN = D / 16, kT = D / 32, kAhead = 4, kExps = 16 / kN;
+                const float base = base_of(x.m);
+                const char *const bk = lk + (next_buf * kKeys + kHalf * next_b) * Sh::kRow;
+                const char *const bv = lv + (buf * kKeys + kHalf * b) * Sh::kRow;
+                u32x4_t kf[kAhead], vf[2][kT], pk[2];
+                float pr[16], l[2], big = 0.0f;
+                auto read_k = [&](int i) { kf[i % kAhead] = tl::ld16(bk + ((2 * i + h) ^ tk) * 16); };
+                auto read_v = [&](int c, int j) {
+                    const char *const at = bv + 16 * c * Sh::kRow + ((4 * j + vchunk) ^ tv) * 16;
+                    const uint2 lo = read_transposed(at), hi = read_transposed(at + 8 * Sh::kRow);
+                    vf[c][j] = u32x4_t{lo.x, lo.y, hi.x, hi.y};
+                };
+                auto pack = [&](int c) {
+                    const float *const e = pr + 8 * c;
+                    l[c] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                    pk[c] = u32x4_t{tl::pack_bf16x2(e[0], e[1]), tl::pack_bf16x2(e[2], e[3]), tl::pack_bf16x2(e[4], e[5]),
+                                    tl::pack_bf16x2(e[6], e[7])};
+                };
+                next = f32x16_t{};
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) read_k(i);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < kN; ++i) {
+                    next = mfma_32x32x16(kf[i % kAhead], q[i], next);
+                    if (i + kAhead < kN) read_k(i + kAhead);
+                    if (i >= kN - kT) read_v(0, i - (kN - kT));
+#pragma unroll
+                    for (int e = i * kExps; e < (i + 1) * kExps; ++e) pr[e] = exp2_fast(fmaf(s[e], cf, -base));
+                    if ((i + 1) * kExps == 8) pack(0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < kT; ++j) {
+                        x.o[j] = mfma_32x32x16(vf[c][j], pk[c], x.o[j]);
+                        if (c == 0) {
+                            read_v(1, j);
+                            if (j == 0) pack(1);
+                        } else {
+#pragma unroll
+                            for (int e = j * (16 / kT); e < (j + 1) * (16 / kT); ++e)
+                                big = e == 0 ? next[0] : larger(big, next[e]);
+                            if (j == 0) x.l += l[0] + l[1];
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                return big;
+            };
+            // The builtin, since the compiler counts what it waits for: it would
+            // otherwise wait for the rows of q in the loop, and so for the next keys.
+            auto arrive = [&]() {
                 __builtin_amdgcn_s_waitcnt(kWaitLoads);
                 __syncthreads();
-                const bool more = k0 + kKeys < p.hi;
-                if (more) {
-                    start(k0 + kKeys, buf ^ 1);
-                    pages(k0 + 2 * kKeys);
+            };
+
+            // Rounds of 64 keys.  Before round k0 the buffers of K hold or are being sent
+            // the keys from k0 - 32 and from k0 + 32, that of V those from k0.
+            if (p.lo < p.hi) {
+                pages(p.lo - kHalf, k_page);
+                pages(p.lo, v_page);
+                start_k(p.lo, 0);
+                store_k(p.lo, 0);
+                start_v(p.lo, 0);
+                store_v(p.lo, 0);
+                start_k(p.lo + kKeys, 1);
+                store_k(p.lo + kKeys, 1);
+            }
+            int k0 = p.lo;
+            if constexpr (!kCareful) {
+                // Keys that all rows see: scores 32 keys ahead, so that products and
+                // exponentials, which different units compute, have something of the other
+                // to run beside.
+                const int full = p.lo + max(0, min(p.hi, tile_all_see) - p.lo) / kKeys * kKeys;
+                if (k0 < full) {
+                    f32x16_t s0, s1;
+                    float big = 0.0f;
+                    arrive();
+                    if (any) {
+                        s0 = scores(0, 1);
+                        big = largest(s0);
+                    }
+                    auto step = [&](auto buffer) {
+                        constexpr int buf = decltype(buffer)::value;
+                        const bool more = k0 + kKeys < full;
+                        arrive();
+                        start_v(k0 + kKeys, buf ^ 1);
+                        start_k(k0 + 2 * kKeys, buf);
+                        if (any) {
+                            rescale(big);
+                            big = mixed(s0, buf, 0, s1, buf ^ 1, 0);
+                            rescale(big);
+                            big = mixed(s1, buf, 1, s0, buf ^ 1, 1);  // (the latter's not used after the last round)
+                        }
+                        store_v(k0 + kKeys, buf ^ 1);
+                        store_k(k0 + 2 * kKeys, buf);
+                        k0 += kKeys;
+                        return more;
+                    };
+#pragma unroll 1
+                    while (step(std::integral_constant<int, 0>{}) && step(std::integral_constant<int, 1>{})) {
+                    }
                 }
-                if (k0 < wave_sees) round(k0, buf);
-                if (more) store(buf ^ 1);
+            }
+            // The rest, whose scores are masked.
+#pragma unroll 1
+            for (; k0 < p.hi; k0 += kKeys) {
+                const int buf = (k0 - p.lo) / kKeys & 1;
+                arrive();
+                start_v(k0 + kKeys, buf ^ 1);
+                f32x16_t s[2];
+                const bool busy = k0 < wave_sees;
+                if (busy) {
+                    uint64_t absent[2] = {};
+                    if constexpr (kCareful)
+                        for (int k = 0; k < kWaves; ++k) {
+                            absent[0] |= sh.absent[buf][k] >> 32;
+                            absent[1] |= sh.absent[buf ^ 1][k];
+                        }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const int left = seen - k0 - kHalf * b - 4 * h;
+                        if (k0 + kHalf * b >= p.hi) {  // (not even sent)
+                            for (int i = 0; i < 16; ++i) s[b][i] = -INFINITY;
+                            continue;
+                        }
+                        s[b] = scores(buf ^ b, b ^ 1);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int key = 8 * (i / 4) + i % 4;
+                            if (key >= left || (kCareful && ((absent[b] >> (key + 4 * h)) & 1))) s[b][i] = -INFINITY;
+                        }
+                    }
+                }
+                __syncthreads();  // (the first keys are read by all)
+                start_k(k0 + 2 * kKeys, buf);
+                if (busy) {
+                    rescale(larger(largest(s[0]), largest(s[1])));
+                    add(s[0], buf, 0);
+                    add(s[1], buf, 1);
+                    if constexpr (kCareful) {
+#pragma unroll 1
+                        for (int key = 0; key < kKeys; ++key) {
+                            const char *const at = sh.v[buf] + key * Sh::kRow + 8 * h;
+#pragma unroll
+                            for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint2 v =
+                                        *reinterpret_cast<const uint2 *>(at + ((4 * j + i) ^ Sh::v_turn(key)) * 16);
+                                    float f[4] = {};
+                                    add_not_finite(f, v, k0 + key < seen);
+                                    for (int e = 0; e < 4; ++e) x.o[j][4 * i + e] += f[e];
+                                }
+                        }
+                    }
+                }
+                store_v(k0 + kKeys, buf ^ 1);
+                store_k(k0 + 2 * kKeys, buf);
             }
             x.l += __shfl_xor(x.l, 32);
             if constexpr (kCareful) return false;
@@ -437,17 +615,27 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
     }
 }
 
+template <int D, bool F8>
+void launch_rows(const AttendArgs &a, hipStream_t st) {
+    const dim3 grid(a.groups_of_threads), block(kThreads);
+    constexpr int kOfLoad = kKeysOfLoad<D, F8>;
+    // (with the lane's offset in 32 bits)
+    if (a.cache.page % kOfLoad == 0 && a.token_units < (1u << 31) / (16 * kOfLoad))
+        attend_many_kernel<D, F8, true><<<grid, block, 0, st>>>(a);
+    else
+        attend_many_kernel<D, F8, false><<<grid, block, 0, st>>>(a);
+}
+
 template <int D>
 hipError_t go(const AttendArgs &a, hipStream_t st) {
-    const dim3 grid(a.groups_of_threads), block(kThreads);
     if (a.cache.k_scale)
-        attend_many_kernel<D, true><<<grid, block, 0, st>>>(a);
+        launch_rows<D, true>(a, st);
     else
-        attend_many_kernel<D, false><<<grid, block, 0, st>>>(a);
+        launch_rows<D, false>(a, st);
     if (hipError_t e = hipGetLastError()) return e;
     // (no tile that the table allows is worth cutting)
     if (kTileCost + (int64_t)a.table_cols * a.cache.page <= kManyWhole) return hipSuccess;
-    attend_join_kernel<D><<<dim3(kJoinGroups), block, 0, st>>>(a);
+    attend_join_kernel<D><<<dim3(kJoinGroups), dim3(kThreads), 0, st>>>(a);
     return hipGetLastError();
 }
 
