@@ -102,8 +102,8 @@ __device__ __forceinline__ const int32_t *table_of(const AttendArgs &a, int j) {
     const int row = a.groups ? min(max(j - 1, 0), a.jobs - 3) : j;
     return a.table + row * a.ld_table;
 }
-__device__ __forceinline__ int64_t job_cost(const AttendArgs &a, Span s, int tokens) {
-    return tiles_cost(s, tokens, a.causal, tiles_of(s.rows, tokens));
+__device__ __forceinline__ int64_t job_cost(const AttendArgs &a, Span s, int tokens, int fixed) {
+    return tiles_cost(s, tokens, a.causal, fixed, tiles_of(s.rows, tokens));
 }
 
 // Neighbouring ranges, which share keys, go to one XCD.
@@ -129,13 +129,14 @@ struct Walk {
     Job job;
 
     // By every thread of the workgroup; false if nothing is left for it.
-    __device__ __forceinline__ bool find(const AttendArgs &a, int rows, int least, int whole, Found &found) {
+    __device__ __forceinline__ bool find(const AttendArgs &a, int rows, int fixed, int least, int whole,
+                                         Found &found) {
         const int tid = threadIdx.x, lane = tl::lane_id();
         tokens = scalar(rows / a.each);
         w = workgroup_of(a);
         const int per = (a.jobs + kThreads - 1) / kThreads, j0 = min(tid * per, a.jobs), j1 = min(j0 + per, a.jobs);
         int64_t mine = 0;
-        for (int k = j0; k < j1; ++k) mine += a.kv * job_cost(a, job_of(a, k).s, tokens);
+        for (int k = j0; k < j1; ++k) mine += a.kv * job_cost(a, job_of(a, k).s, tokens, fixed);
         int64_t incl = mine;
         for (int d = 1; d < kWave; d *= 2) {
             const int64_t up = __shfl_up((long long)incl, d);
@@ -149,8 +150,8 @@ struct Walk {
             total += found.wave_sum[k];
         }
         total = scalar64(total);
-        r = ranges_of(total, a.groups_of_threads, least, whole);
-        r = {scalar64(r.size), scalar64(r.whole)};
+        r = ranges_of(total, a.groups_of_threads, fixed, least, whole);
+        r = {scalar64(r.size), scalar64(r.whole), fixed};
         const int64_t begin = w * r.size;
         end = begin + r.size < total ? begin + r.size : total;
         if (begin >= total) return false;
@@ -158,7 +159,7 @@ struct Walk {
             int64_t base = incl - mine;
             int k = j0;
             for (;; ++k) {
-                const int64_t c = a.kv * job_cost(a, job_of(a, k).s, tokens);
+                const int64_t c = a.kv * job_cost(a, job_of(a, k).s, tokens, fixed);
                 if (begin < base + c) break;
                 base += c;
             }
@@ -168,10 +169,10 @@ struct Walk {
         __syncthreads();
         j = scalar(found.job);
         load(a);
-        const int64_t base = scalar64(found.base), head = scalar64(job_cost(a, job.s, tokens));
+        const int64_t base = scalar64(found.base), head = scalar64(job_cost(a, job.s, tokens, fixed));
         g = scalar((int)((begin - base) / head));
-        i = scalar(tile_at(job.s, tokens, a.causal, begin - base - g * head));
-        at = scalar64(base + g * head + tiles_cost(job.s, tokens, a.causal, i));
+        i = scalar(tile_at(job.s, tokens, a.causal, fixed, begin - base - g * head));
+        at = scalar64(base + g * head + tiles_cost(job.s, tokens, a.causal, fixed, i));
         return true;
     }
     __device__ __forceinline__ void load(const AttendArgs &a) {
@@ -189,7 +190,7 @@ struct Walk {
     }
     // The next tile; false behind the range's last one.
     __device__ __forceinline__ bool next(const AttendArgs &a) {
-        at += kTileCost + keys(a);
+        at += r.fixed + keys(a);
         if (at >= end) return false;
         if (++i < tiles) return true;
         i = 0;

@@ -66,8 +66,8 @@ AttendPlan attend_plan(int n, int heads, int dim, bool prefixes) {
 
 // Workgroups for a call: no more than the chip holds at once, nor than there
 // are least ranges in the most that the tables allow.
-int groups_for(int64_t tiles, int64_t keys, int least, int most) {
-    const int64_t g = (tiles * (st::kTileCost + keys) + least - 1) / least;
+int groups_for(int64_t tiles, int64_t cost, int least, int most) {
+    const int64_t g = (tiles * cost + least - 1) / least;
     return g < 1 ? 1 : g > most ? most : (int)g;
 }
 
@@ -77,8 +77,8 @@ hipError_t launch(st::AttendArgs &a, int64_t rows_of_job, hipStream_t stream) {
     const bool few = a.each <= st::kFewRows && rows_of_job * a.each <= st::kFewRows;
     const int tokens = (few ? st::kFewRows : st::kManyRows) / a.each;
     const int64_t tiles = ((int64_t)a.n / tokens + a.jobs) * a.kv, keys = (int64_t)a.table_cols * a.cache.page;
-    a.groups_of_threads = few ? groups_for(tiles, keys, st::kFewLeast, few_groups(a.dim))
-                              : groups_for(tiles, keys, st::kManyLeast, many_groups(a.dim));
+    a.groups_of_threads = few ? groups_for(tiles, st::kFewFixed + keys, st::kFewLeast, few_groups(a.dim))
+                              : groups_for(tiles, st::kManyFixed + keys, st::kManyLeast, many_groups(a.dim));
     return few ? st::launch_attend_few(a, stream) : st::launch_attend_many(a, stream);
 }
 

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_few_kernel(A
     constexpr int kLanes = D * kSize / 16, kRows = kWave / kLanes, kLoads = kKeys / kRows;  // lanes of a key; keys of a load
     __shared__ Sh sh;
     Walk w;
-    if (!w.find(a, kFewRows, kFewLeast, kFewWhole, sh.found)) return;
+    if (!w.find(a, kFewRows, kFewFixed, kFewLeast, kFewWhole, sh.found)) return;
     const int lane = tl::lane_id(), wave = scalar(tl::wave_id()), h = lane / 16, r = lane % 16;
     char *const lk = sh.wave[wave], *const lv = lk + kKeys * Sh::kK;
     const int lc = lane % kLanes, lr = lane / kLanes;      // this lane's chunk and row of a load

@@ -42,8 +42,6 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t st);
 // one belongs to the workgroup that its middle falls to.
 // Everything follows from the lengths, so the device divides by itself and a
 // captured call follows lengths that change.
-constexpr int kTileCost = 64;
-
 struct Span {
     int rows, len;
 };
@@ -55,26 +53,25 @@ __host__ __device__ inline int tile_keys(Span s, int tokens, bool causal, int i)
     return e > 0 ? (int)e : 0;
 }
 // Cost of the first m tiles of a request and one key head.
-__host__ __device__ inline int64_t tiles_cost(Span s, int tokens, bool causal, int m) {
-    const int64_t fixed = (int64_t)m * kTileCost;
-    if (!causal) return fixed + (int64_t)m * s.len;
+__host__ __device__ inline int64_t tiles_cost(Span s, int tokens, bool causal, int fixed, int m) {
+    if (!causal) return (int64_t)m * (fixed + s.len);
     const bool all = m > 0 && m == tiles_of(s.rows, tokens);
     const int64_t full = all ? m - 1 : m, a = (int64_t)s.len - s.rows;
     int64_t none = a >= 0 ? 0 : -a / tokens;  // tiles that see nothing
     if (none > full) none = full;
     const int64_t count = full - none;
-    return fixed + count * a + tokens * (count * (none + 1 + full) / 2) + (all ? s.len : 0);
+    return (int64_t)m * fixed + count * a + tokens * (count * (none + 1 + full) / 2) + (all ? s.len : 0);
 }
 // The tile that holds cost offset `at` < tiles_cost(all).
-__host__ __device__ inline int tile_at(Span s, int tokens, bool causal, int64_t at) {
+__host__ __device__ inline int tile_at(Span s, int tokens, bool causal, int fixed, int64_t at) {
     int lo = 0, hi = tiles_of(s.rows, tokens) - 1;
     if (!causal) {
-        const int64_t i = at / (kTileCost + s.len);
+        const int64_t i = at / (fixed + s.len);
         return i < hi ? (int)i : hi;
     }
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (tiles_cost(s, tokens, causal, mid) <= at)
+        if (tiles_cost(s, tokens, causal, fixed, mid) <= at)
             lo = mid;
         else
             hi = mid - 1;
@@ -84,11 +81,12 @@ __host__ __device__ inline int tile_at(Span s, int tokens, bool causal, int64_t 
 // A workgroup's range, and which part of a tile belongs to it.
 struct Ranges {
     int64_t size, whole;
+    int fixed;
 };
-__host__ __device__ inline Ranges ranges_of(int64_t total, int groups, int least, int whole) {
+__host__ __device__ inline Ranges ranges_of(int64_t total, int groups, int fixed, int least, int whole) {
     int64_t size = (total + groups - 1) / groups;
     if (size < least) size = least;
-    return {size, size / 4 > whole ? size / 4 : whole};
+    return {size, size / 4 > whole ? size / 4 : whole, fixed};
 }
 struct Piece {
     bool mine, split, begins;  // (begins: with the tile's first key)
@@ -99,7 +97,7 @@ struct Piece {
 // The part of the tile at cost `at` with `keys` keys that workgroup w computes;
 // pieces begin at multiples of `step` keys.
 __host__ __device__ inline Piece piece_of(const Ranges &r, int w, int64_t at, int keys, int step) {
-    const int64_t cost = kTileCost + keys, u0 = w * r.size, u1 = u0 + r.size;
+    const int64_t cost = r.fixed + keys, u0 = w * r.size, u1 = u0 + r.size;
     Piece p{};
     if (cost <= r.whole) {
         const int64_t mid = at + cost / 2;
@@ -111,7 +109,7 @@ __host__ __device__ inline Piece piece_of(const Ranges &r, int w, int64_t at, in
     p.mine = at < u1 && at + cost > u0;
     if (!p.mine) return p;
     p.begins = at >= u0;
-    const int64_t lo = u0 > at ? u0 - at - kTileCost : 0, hi = u1 - at - kTileCost;
+    const int64_t lo = u0 > at ? u0 - at - r.fixed : 0, hi = u1 - at - r.fixed;
     p.lo = lo > 0 ? (int)(lo / step * step) : 0;
     p.hi = u1 >= at + cost ? keys : hi > 0 ? (int)(hi / step * step) : 0;
     p.first = (int)(at / r.size);
@@ -128,7 +126,8 @@ constexpr int kFewRows = 16, kManyRows = 128;  // rows of a tile: of few rows, o
 constexpr int kMaxEach = 64;                   // query heads of a key head
 constexpr int kMaxDim = 256;
 constexpr int kFewGroups = 768, kManyGroups = 512;  // workgroups at most
-constexpr int kFewLeast = 128, kManyLeast = 128;     // the least range of one
+constexpr int kFewFixed = 64, kManyFixed = 256;      // what a tile costs beside its keys, in keys
+constexpr int kFewLeast = 128, kManyLeast = 256;     // the least range of a workgroup
 constexpr int kFewWhole = 256, kManyWhole = 1024;    // a tile of no more is not cut
 constexpr int kFewStep = 128, kManyStep = 64;        // keys of a round
 constexpr int kJoinGroups = 512;                     // workgroups that join pieces of many rows

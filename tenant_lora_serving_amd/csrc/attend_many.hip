@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
     __shared__ Sh sh;
     Walk w;
     if (threadIdx.x == 0) a.joins[workgroup_of(a)].pieces = 0;
-    if (!w.find(a, kManyRows, kManyLeast, kManyWhole, sh.found)) return;
+    if (!w.find(a, kManyRows, kManyFixed, kManyLeast, kManyWhole, sh.found)) return;
     const int lane = tl::lane_id(), wave = scalar(tl::wave_id()), h = lane / 32;
     // this lane's key of load u is (u * kWaves + wave) * kOfWave + lr
     const int lc = lane % kLanes, lr = lane / kLanes;
@@ -190,43 +190,55 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
             }
             bool met = false;
             u32x4_t kr[F8 ? kLoads : 1], vr[F8 ? kLoads : 1];
-            // Pages of 64 keys' tokens, looked up a round ahead.  K is taken 32 keys
-            // before V, from k0 - 32.
-            int k_page[kLoads], v_page[kLoads];
-            auto key_in = [&](int k0, int u) { return k0 + (kQuick ? (u * kWaves + wave) * kOfWave : key_of(u)); };
-            auto pages = [&](int k0, int (&page)[kLoads]) {
+            // Round k0 sends for V's keys k0 + 64 .. and K's k0 + 96 ..; their pages are looked up
+            // a round before.  In even pages lane i works out the place of the i-th load
+            // instruction's keys, first those of V, then of K: a few vector instructions
+            // for all of them, where scalar ones for each took longer than the loads.
+            constexpr int kAhead[2] = {kKeys, kKeys + kHalf};
+            int page[kQuick ? 1 : 2 * kLoads];
+            const char *place = nullptr;
+            auto first_key = [&](int k0, int i) {  // of load i's keys; of the lane's, where each has its own
+                const int u = (i % kLoads * kWaves + wave) * kOfWave + (kQuick ? 0 : lr);
+                return k0 + (i < kLoads ? kAhead[0] : kAhead[1]) + u;
+            };
+            auto has = [&](int key) { return key >= p.lo && key < p.hi; };
+            auto look_up = [&](int k0) {
 #pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    const int key = key_in(k0, u);
-                    page[u] = key >= p.lo && key < p.hi ? table[page_of(a.div, key)] : kQuick ? 0 : -1;
+                for (int i = 0; i < (kQuick ? 1 : 2 * kLoads); ++i) {
+                    const int key = first_key(k0, kQuick ? lane % (2 * kLoads) : i);
+                    page[i] = has(key) ? table[page_of(a.div, key)] : kQuick ? 0 : -1;
                 }
             };
-            // One of K and V, 64 keys.  Chunks of absent keys and past the head's columns
-            // are read from zeros: their scores are masked, but an infinity or NaN among
-            // their values would make NaN of p = 0.
-            auto start = [&](int k0, const int (&page)[kLoads], const char *base, char *buf, auto turn, u32x4_t *regs) {
-                const uint32_t lds = lds_address(buf) + wave * kWave * 16;
-                const bool whole = !F8 && kQuick && a.dim == D && k0 >= p.lo && k0 + kKeys <= p.hi;
-                const char *from_u[kLoads];
-                bool known[kLoads];
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    const int page_u = kQuick ? scalar(page[u]) : page[u], key = key_in(k0, u);
-                    const int in_page = key - page_of(a.div, key) * a.cache.page;
-                    known[u] = (uint32_t)page_u < (uint32_t)a.cache.pages;
-                    if constexpr (kQuick) {
-                        met |= !known[u];
-                        from_u[u] = base + token_offset(a, known[u] ? page_u : 0, key >= p.lo ? in_page : 0);
-                    } else {
-                        met |= !known[u] && key >= p.lo && key < p.hi;
-                        from_u[u] = base + token_offset(a, page_u, in_page);
-                    }
+            auto find_places = [&](int k0) {
+                if constexpr (kQuick) {
+                    const int key = first_key(k0, lane % (2 * kLoads)), in_page = key - page_of(a.div, key) * a.cache.page;
+                    const bool known = (uint32_t)page[0] < (uint32_t)a.cache.pages;
+                    met |= !known;
+                    place = (lane % (2 * kLoads) < kLoads ? vh : kh) +
+                            token_offset(a, known ? page[0] : 0, has(key) ? in_page : 0);
                 }
-                if (whole) {
+            };
+            auto place_of = [&](int i) {  // of load i's first key
+                const int64_t at = reinterpret_cast<int64_t>(place);
+                const uint32_t lo = __builtin_amdgcn_readlane((int)at, i), hi = __builtin_amdgcn_readlane((int)(at >> 32), i);
+                return reinterpret_cast<const char *>((uint64_t)hi << 32 | lo);
+            };
+            // Chunks of absent keys and past the head's columns are read from zeros:
+            // their scores are masked, but an infinity or NaN among their values
+            // would make NaN of p = 0.
+            auto send = [&](int k0, auto of_k, char *buf, auto turn, u32x4_t *regs) {
+                constexpr int kFirst = decltype(of_k)::value ? kLoads : 0;
+                const int from_key = k0 + kAhead[decltype(of_k)::value ? 1 : 0];
+                const uint32_t lds = lds_address(buf) + wave * kWave * 16;
+                if (kQuick && a.dim == D && from_key >= p.lo && from_key + kKeys <= p.hi) {
 #pragma unroll
-                    for (int u = 0; u < kLoads; ++u)
-                        load_lds(reinterpret_cast<const char *>(scalar64(reinterpret_cast<int64_t>(from_u[u]))),
-                                 from + (lc ^ turn(key_of(u))) * 16, lds + u * kThreads * 16);
+                    for (int u = 0; u < kLoads; ++u) {
+                        const char *const base = place_of(kFirst + u);
+                        if constexpr (F8)
+                            regs[u] = tl::ld16(base + (from + lc * 16));
+                        else
+                            load_lds(base, from + (lc ^ turn(key_of(u))) * 16, lds + u * kThreads * 16);
+                    }
                     return;
                 }
                 // (places worked out here, not kept in registers through the rounds that do without)
@@ -236,14 +248,23 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
                 for (int u = 0; u < kLoads; ++u) {
                     const int key = (u * kWaves + wave) * kOfWave + l / kLanes;
                     const int chunk = F8 ? l % kLanes : l % kLanes ^ turn(key);
-                    const bool there =
-                        k0 + key >= p.lo && k0 + key < p.hi && known[u] && chunk < a.dim * kSize / 16;
-                    const uint32_t in_load = kQuick ? l / kLanes * a.token_units * 16 : 0;
-                    const char *const at_u = there ? from_u[u] + in_load + chunk * 16 : a.zeros;
+                    bool there = has(from_key + key) && chunk < a.dim * kSize / 16;
+                    const char *at;
+                    if constexpr (kQuick) {
+                        at = place_of(kFirst + u) + l / kLanes * a.token_units * 16;
+                    } else {
+                        const int of = page[kFirst + u], in_page =
+                            from_key + key - page_of(a.div, from_key + key) * a.cache.page;
+                        const bool known = (uint32_t)of < (uint32_t)a.cache.pages;
+                        met |= !known && has(from_key + key);
+                        there = there && known;
+                        at = (decltype(of_k)::value ? kh : vh) + token_offset(a, of, in_page);
+                    }
+                    at = there ? at + chunk * 16 : a.zeros;
                     if constexpr (F8)
-                        regs[u] = tl::ld16(at_u);
+                        regs[u] = tl::ld16(at);
                     else
-                        load_lds(at_u, lds + u * kThreads * 16);
+                        load_lds(at, lds + u * kThreads * 16);
                 }
             };
             auto store = [&](char *buf, auto turn, const u32x4_t *regs) {
@@ -257,31 +278,29 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
             };
             auto k_turn = [](int key) { return Sh::k_turn(key); };
             auto v_turn = [](int key) { return Sh::v_turn(key); };
-            auto start_k = [&](int k0, int buf) {
-                if (k0 - kHalf >= p.hi) return;
-                start(k0 - kHalf, k_page, kh, sh.k[buf], k_turn, kr);
+            // In round k0, whose buffer is buf: for V into the other buffer, for K into this one.
+            auto send_v = [&](int k0, int buf) {
+                if (k0 + kAhead[0] < p.hi) send(k0, std::false_type{}, sh.v[buf ^ 1], v_turn, vr);
+            };
+            auto send_k = [&](int k0, int buf) {
+                if (k0 + kAhead[1] >= p.hi) return;
+                send(k0, std::true_type{}, sh.k[buf], k_turn, kr);
                 if constexpr (kCareful) {  // one bit a key, from the first of its lanes
                     uint64_t absent = 0;
 #pragma unroll
                     for (int u = 0; u < kLoads; ++u) {
-                        const uint64_t bits = __ballot((uint32_t)k_page[u] >= (uint32_t)a.cache.pages);
+                        const uint64_t bits = __ballot((uint32_t)page[kLoads + u] >= (uint32_t)a.cache.pages);
                         for (int e = 0; e < kOfWave; ++e)
                             absent |= ((bits >> (e * kLanes)) & 1) << ((u * kWaves + wave) * kOfWave + e);
                     }
                     if (lane == 0) sh.absent[buf][wave] = absent;
                 }
-                pages(k0 + kHalf, k_page);
-            };
-            auto start_v = [&](int k0, int buf) {
-                if (k0 >= p.hi) return;
-                start(k0, v_page, vh, sh.v[buf], v_turn, vr);
-                pages(k0 + kKeys, v_page);
-            };
-            auto store_k = [&](int k0, int buf) {
-                if (F8 && k0 - kHalf < p.hi) store(sh.k[buf], k_turn, kr);
             };
             auto store_v = [&](int k0, int buf) {
-                if (F8 && k0 < p.hi) store(sh.v[buf], v_turn, vr);
+                if (F8 && k0 + kAhead[0] < p.hi) store(sh.v[buf ^ 1], v_turn, vr);
+            };
+            auto store_k = [&](int k0, int buf) {
+                if (F8 && k0 + kAhead[1] < p.hi) store(sh.k[buf], k_turn, kr);
             };
             // Scores of the lane's row with 32 keys: 8 (i / 4) + 4 h + i % 4 in register i.
             // b: which half of the buffer.
@@ -409,14 +428,17 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
             // Rounds of 64 keys.  Before round k0 the buffers of K hold or are being sent
             // the keys from k0 - 32 and from k0 + 32, that of V those from k0.
             if (p.lo < p.hi) {
-                pages(p.lo - kHalf, k_page);
-                pages(p.lo, v_page);
-                start_k(p.lo, 0);
-                store_k(p.lo, 0);
-                start_v(p.lo, 0);
-                store_v(p.lo, 0);
-                start_k(p.lo + kKeys, 1);
-                store_k(p.lo + kKeys, 1);
+                look_up(p.lo - 2 * kKeys);
+                find_places(p.lo - 2 * kKeys);
+                send_k(p.lo - 2 * kKeys, 0);
+                store_k(p.lo - 2 * kKeys, 0);
+                look_up(p.lo - kKeys);
+                find_places(p.lo - kKeys);
+                send_v(p.lo - kKeys, 1);
+                store_v(p.lo - kKeys, 1);
+                send_k(p.lo - kKeys, 1);
+                store_k(p.lo - kKeys, 1);
+                look_up(p.lo);
             }
             int k0 = p.lo;
             if constexpr (!kCareful) {
@@ -436,16 +458,18 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
                         constexpr int buf = decltype(buffer)::value;
                         const bool more = k0 + kKeys < full;
                         arrive();
-                        start_v(k0 + kKeys, buf ^ 1);
-                        start_k(k0 + 2 * kKeys, buf);
+                        find_places(k0);
+                        send_v(k0, buf);
+                        send_k(k0, buf);
+                        look_up(k0 + kKeys);
                         if (any) {
                             rescale(big);
                             big = mixed(s0, buf, 0, s1, buf ^ 1, 0);
                             rescale(big);
                             big = mixed(s1, buf, 1, s0, buf ^ 1, 1);  // (the latter's not used after the last round)
                         }
-                        store_v(k0 + kKeys, buf ^ 1);
-                        store_k(k0 + 2 * kKeys, buf);
+                        store_v(k0, buf);
+                        store_k(k0, buf);
                         k0 += kKeys;
                         return more;
                     };
@@ -459,7 +483,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
             for (; k0 < p.hi; k0 += kKeys) {
                 const int buf = (k0 - p.lo) / kKeys & 1;
                 arrive();
-                start_v(k0 + kKeys, buf ^ 1);
+                find_places(k0);
+                send_v(k0, buf);
                 f32x16_t s[2];
                 const bool busy = k0 < wave_sees;
                 if (busy) {
@@ -485,7 +510,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
                     }
                 }
                 __syncthreads();  // (the first keys are read by all)
-                start_k(k0 + 2 * kKeys, buf);
+                send_k(k0, buf);
+                look_up(k0 + kKeys);
                 if (busy) {
                     rescale(larger(largest(s[0]), largest(s[1])));
                     add(s[0], buf, 0);
@@ -507,8 +533,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
                         }
                     }
                 }
-                store_v(k0 + kKeys, buf ^ 1);
-                store_k(k0 + 2 * kKeys, buf);
+                store_v(k0, buf);
+                store_k(k0, buf);
             }
             x.l += __shfl_xor(x.l, 32);
             if constexpr (kCareful) return false;
@@ -634,7 +660,7 @@ hipError_t go(const AttendArgs &a, hipStream_t st) {
         launch_rows<D, false>(a, st);
     if (hipError_t e = hipGetLastError()) return e;
     // (no tile that the table allows is worth cutting)
-    if (kTileCost + (int64_t)a.table_cols * a.cache.page <= kManyWhole) return hipSuccess;
+    if (kManyFixed + (int64_t)a.table_cols * a.cache.page <= kManyWhole) return hipSuccess;
     attend_join_kernel<D><<<dim3(kJoinGroups), dim3(kThreads), 0, st>>>(a);
     return hipGetLastError();
 }

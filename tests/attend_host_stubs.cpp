@@ -36,15 +36,15 @@ int stub_page_of(int page, int key) { return st::page_of(st::page_div(page), key
 // The pieces of a call: 12 numbers each (workgroup, job, head, tile, keys of the
 // tile, lo, hi, begins, split, first, count, slot); returns how many there are,
 // or -1 if `most` is too small.
-int stub_divide(int jobs, const int *rows, const int *lens, int kv, int tokens, int causal, int groups, int least,
+int stub_divide(int jobs, const int *rows, const int *lens, int kv, int tokens, int causal, int groups, int fixed, int least,
                 int whole, int step, int *to, int most) {
     auto cost_of = [&](int j) {
         const st::Span s{rows[j], lens[j]};
-        return st::tiles_cost(s, tokens, causal, st::tiles_of(s.rows, tokens));
+        return st::tiles_cost(s, tokens, causal, fixed, st::tiles_of(s.rows, tokens));
     };
     int64_t total = 0;
     for (int j = 0; j < jobs; ++j) total += kv * cost_of(j);
-    const st::Ranges r = st::ranges_of(total, groups, least, whole);
+    const st::Ranges r = st::ranges_of(total, groups, fixed, least, whole);
     int n = 0;
     for (int w = 0; w < groups; ++w) {
         const int64_t begin = w * r.size, end = begin + r.size < total ? begin + r.size : total;
@@ -54,8 +54,8 @@ int stub_divide(int jobs, const int *rows, const int *lens, int kv, int tokens, 
         while (begin >= base + kv * cost_of(j)) base += kv * cost_of(j++);
         const int64_t head = cost_of(j);
         int g = (int)((begin - base) / head);
-        int i = st::tile_at({rows[j], lens[j]}, tokens, causal, begin - base - g * head);
-        int64_t at = base + g * head + st::tiles_cost({rows[j], lens[j]}, tokens, causal, i);
+        int i = st::tile_at({rows[j], lens[j]}, tokens, causal, fixed, begin - base - g * head);
+        int64_t at = base + g * head + st::tiles_cost({rows[j], lens[j]}, tokens, causal, fixed, i);
         for (;;) {
             const st::Span s{rows[j], lens[j]};
             const int keys = st::tile_keys(s, tokens, causal, i);
@@ -68,7 +68,7 @@ int stub_divide(int jobs, const int *rows, const int *lens, int kv, int tokens, 
                 for (int k = 0; k < 12; ++k) to[12 * n + k] = v[k];
                 ++n;
             }
-            at += st::kTileCost + keys;
+            at += fixed + keys;
             if (at >= end) break;
             if (++i < st::tiles_of(s.rows, tokens)) continue;
             i = 0;

@@ -172,17 +172,18 @@ def test_page_of(L):
 
 
 # ---------------------------------------------------------------- division
-def divide(L, rows, lens, kv, tokens, causal, groups, least, whole, step):
+def divide(L, rows, lens, kv, tokens, causal, groups, least, whole, step, fixed):
     arr = ctypes.c_int * len(rows)
     most = 200000
     to = (ctypes.c_int * (12 * most))()
-    n = L.stub_divide(len(rows), arr(*rows), arr(*lens), kv, tokens, causal, groups, least, whole, step, to, most)
+    n = L.stub_divide(len(rows), arr(*rows), arr(*lens), kv, tokens, causal, groups, fixed, least, whole, step, to,
+                      most)
     assert n >= 0
     return [tuple(to[12 * k:12 * k + 12]) for k in range(n)]
 
 
-def check_division(L, rows, lens, kv, tokens, causal, groups, least, whole, step):
-    pieces = divide(L, rows, lens, kv, tokens, causal, groups, least, whole, step)
+def check_division(L, rows, lens, kv, tokens, causal, groups, least, whole, step, fixed=64):
+    pieces = divide(L, rows, lens, kv, tokens, causal, groups, least, whole, step, fixed)
     by_tile, slots, tickets = {}, set(), {}
     for w, j, g, i, keys, lo, hi, begins, split, first, count, slot in pieces:
         by_tile.setdefault((j, g, i), []).append((w, keys, lo, hi, begins, split, first, count, slot))
@@ -198,7 +199,7 @@ def check_division(L, rows, lens, kv, tokens, causal, groups, least, whole, step
             assert keys == see and lo == at and lo <= hi and (hi == keys or hi % step == 0)
             at = hi
             assert bool(begins) == (w == parts[0][0]) and bool(split) == (len(parts) > 1)
-            per_group[w] = per_group.get(w, 0) + hi - lo + 64
+            per_group[w] = per_group.get(w, 0) + hi - lo + fixed
             if split:
                 assert first == parts[0][0] and count == len(parts)
                 assert slot >= 0 and slot // 2 == w and slot not in slots
@@ -220,7 +221,8 @@ def test_division_covers_every_key_once(L, seed):
     kv, tokens = rng.choice([1, 2, 8]), rng.choice([1, 4, 5, 16, 32, 128])
     few = rng.random() < 0.5
     groups = rng.choice([1, 2, 7, 64, 512])
-    check_division(L, rows, lens, kv, tokens, causal, groups, 128, 256 if few else 1024, 128 if few else 64)
+    check_division(L, rows, lens, kv, tokens, causal, groups, 128, 256 if few else 1024, 128 if few else 64,
+                   rng.choice([64, 256]))
 
 
 def test_division_is_even(L):
