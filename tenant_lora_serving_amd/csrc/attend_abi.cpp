@@ -77,7 +77,7 @@ hipError_t launch(st::AttendArgs &a, int64_t rows_of_job, hipStream_t stream) {
     const bool few = a.each <= st::kFewRows && rows_of_job * a.each <= st::kFewRows;
     const int tokens = (few ? st::kFewRows : st::kManyRows) / a.each;
     const int64_t tiles = ((int64_t)a.n / tokens + a.jobs) * a.kv, keys = (int64_t)a.table_cols * a.cache.page;
-    a.groups_of_threads = few ? groups_for(tiles, st::kFewFixed + keys, st::kFewLeast, few_groups(a.dim))
+    a.groups_of_threads = few ? groups_for(tiles, (a.cache.k_scale ? st::kFewFixed8 : st::kFewFixed) + keys, st::kFewLeast, few_groups(a.dim))
                               : groups_for(tiles, st::kManyFixed + keys, st::kManyLeast, many_groups(a.dim));
     return few ? st::launch_attend_few(a, stream) : st::launch_attend_many(a, stream);
 }

@@ -86,7 +86,7 @@ __device__ __forceinline__ void few_join(const AttendArgs &a, const Walk &w, con
         const int r = e / (D / 4), c = e % (D / 4) * 4;
         float m = -INFINITY, l = 0.0f;
         f32x4_t o = {};
-        constexpr int kAt = 4;
+        constexpr int kAt = 8;
         for (int k0 = wave; k0 < p.count; k0 += kWaves * kAt) {
             float2 ml[kAt], lo[kAt], hi[kAt];
 #pragma unroll
@@ -114,13 +114,13 @@ __device__ __forceinline__ void few_join(const AttendArgs &a, const Walk &w, con
 }
 
 template <int D, bool F8>
-__global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void attend_few_kernel(AttendArgs a) {
     using Sh = FewShared<D>;
     constexpr int kSize = F8 ? 1 : 2, kKeys = Sh::kKeys;
     constexpr int kLanes = D * kSize / 16, kRows = kWave / kLanes, kLoads = kKeys / kRows;  // lanes of a key; keys of a load
     __shared__ Sh sh;
     Walk w;
-    if (!w.find(a, kFewRows, kFewFixed, kFewLeast, kFewWhole, sh.found)) return;
+    if (!w.find(a, kFewRows, F8 ? kFewFixed8 : kFewFixed, kFewLeast, kFewWhole, sh.found)) return;
     const int lane = tl::lane_id(), wave = scalar(tl::wave_id()), h = lane / 16, r = lane % 16;
     char *const lk = sh.wave[wave], *const lv = lk + kKeys * Sh::kK;
     const int lc = lane % kLanes, lr = lane / kLanes;      // this lane's chunk and row of a load
@@ -201,10 +201,13 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_few_kernel(A
                 if (ok != ~0u && !((ok >> key) & 1)) vr[u] = tl::zero4();
                 char *const ks = lk + key * Sh::kK, *const vs = lv + key * Sh::kV;
                 if constexpr (F8) {
+                    // (of V, odd rows' second half first: a write's 16 bytes then fall on all banks)
+                    const bool odd = lr & 1;
+                    const int at = lc * 32 + (odd ? 16 : 0), other = lc * 32 + (odd ? 0 : 16);
                     tl::st16(ks + lc * 32, widen8(kr[u].x, kr[u].y));
                     tl::st16(ks + lc * 32 + 16, widen8(kr[u].z, kr[u].w));
-                    tl::st16(vs + lc * 32, widen8(vr[u].x, vr[u].y));
-                    tl::st16(vs + lc * 32 + 16, widen8(vr[u].z, vr[u].w));
+                    tl::st16(vs + at, widen8(odd ? vr[u].z : vr[u].x, odd ? vr[u].w : vr[u].y));
+                    tl::st16(vs + other, widen8(odd ? vr[u].x : vr[u].z, odd ? vr[u].y : vr[u].w));
                 } else {
                     tl::st16(ks + lc * 16, kr[u]);
                     tl::st16(vs + lc * 16, vr[u]);

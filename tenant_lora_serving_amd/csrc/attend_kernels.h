@@ -37,7 +37,7 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t st);
 // into tiles of `tokens` rows by `each` heads.  A tile costs kTileCost and the
 // keys that its last row sees.  All tiles' costs one after another, request by
 // request, key head by key head, are cut into equal ranges, one for every
-// workgroup.  A tile that costs more than `whole` is cut where the ranges
+// workgroup.  A tile of more than `whole` keys, or a quarter of a range, is cut where the ranges
 // meet, and its pieces' results go to the workspace and are joined; a smaller
 // one belongs to the workgroup that its middle falls to.
 // Everything follows from the lengths, so the device divides by itself and a
@@ -86,7 +86,7 @@ struct Ranges {
 __host__ __device__ inline Ranges ranges_of(int64_t total, int groups, int fixed, int least, int whole) {
     int64_t size = (total + groups - 1) / groups;
     if (size < least) size = least;
-    return {size, size / 4 > whole ? size / 4 : whole, fixed};
+    return {size, size / 4 > fixed + whole ? size / 4 : fixed + whole, fixed};
 }
 struct Piece {
     bool mine, split, begins;  // (begins: with the tile's first key)
@@ -126,9 +126,11 @@ constexpr int kFewRows = 16, kManyRows = 128;  // rows of a tile: of few rows, o
 constexpr int kMaxEach = 64;                   // query heads of a key head
 constexpr int kMaxDim = 256;
 constexpr int kFewGroups = 768, kManyGroups = 512;  // workgroups at most
-constexpr int kFewFixed = 64, kManyFixed = 256;      // what a tile costs beside its keys, in keys
-constexpr int kFewLeast = 128, kManyLeast = 256;     // the least range of a workgroup
-constexpr int kFewWhole = 256, kManyWhole = 1024;    // a tile of no more is not cut
+// What a tile costs beside its keys, in keys (about 6 us of a workgroup's time;
+// 256 requests over 64 to 4096 keys of 8 bits: 102 us, with 64 for it 135).
+constexpr int kFewFixed = 128, kFewFixed8 = 320, kManyFixed = 256;
+constexpr int kFewLeast = 256, kManyLeast = 256;     // the least range of a workgroup
+constexpr int kFewWhole = 192, kManyWhole = 768;     // a tile of no more keys is not cut
 constexpr int kFewStep = 128, kManyStep = 64;        // keys of a round
 constexpr int kJoinGroups = 512;                     // workgroups that join pieces of many rows
 // A workspace begins with a ticket for every workgroup, 0 between calls, and 16

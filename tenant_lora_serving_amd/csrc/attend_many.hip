@@ -584,21 +584,25 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
 }
 
 // The pieces of split tiles, in their order.  A wave takes 32 rows of a tile and
-// 16 columns of each; the tiles are those that the workgroups before noted.
+// 8 columns of each; the tiles are those that the workgroups before noted.
 template <int D>
 __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
-    constexpr int kPairs = 4, kItems = kWaves * (D / 4 / kPairs);  // of a lane; of a tile
+    constexpr int kPairs = 2, kItems = kWaves * (D / 4 / kPairs);  // of a lane; of a tile
     __shared__ int tiles[kManyGroups], scratch[kWaves + 1];
     const int lane = tl::lane_id(), h = lane / 32;
-    int total = 0;
-    for (int e0 = 0; e0 < a.groups_of_threads; e0 += kThreads) {
-        const int e = e0 + threadIdx.x;
-        const bool split = e < a.groups_of_threads && a.joins[e].pieces > 0;
-        int more;
-        const int at = tl::block_excl_scan<kThreads>(split, scratch, more);
-        if (split) tiles[total + at] = e;
-        total += more;
+    constexpr int kEach = kManyGroups / kThreads;
+    bool split[kEach];
+    int mine = 0, total;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int e = threadIdx.x * kEach + k;
+        split[k] = e < a.groups_of_threads && a.joins[e].pieces > 0;
+        mine += split[k];
     }
+    int at = tl::block_excl_scan<kThreads>(mine, scratch, total);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+        if (split[k]) tiles[at++] = threadIdx.x * kEach + k;
     __syncthreads();
     for (int item = blockIdx.x * kWaves + tl::wave_id(); item < total * kItems; item += gridDim.x * kWaves) {
         const int first = tiles[item / kItems], quarter = item % kItems % kWaves, pair = item % kItems / kWaves * kPairs;
@@ -607,7 +611,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
         if (quarter * 32 >= t.rows) continue;
         float m = -INFINITY, l = 0.0f;
         float2 o[kPairs] = {};
-        constexpr int kAt = 4;
+        constexpr int kAt = 8;
         for (int k0 = 0; k0 < t.pieces; k0 += kAt) {
             float2 ml[kAt], v[kAt][kPairs];
 #pragma unroll
@@ -634,7 +638,7 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
         const int qh = t.g * a.each + r % a.each;
         const float f = result_factor(a, t.g, l);
 #pragma unroll
-        for (int i = 0; i < kPairs; i += 2)
+        for (int i = 0; i < kPairs; i += 2)  // (four columns)
             put_columns(a, row, qh, D, 32 * ((pair + i) / 8) + 8 * ((pair + i) % 8 / 2) + 4 * h, f,
                         f32x4_t{o[i].x, o[i].y, o[i + 1].x, o[i + 1].y});
         if (pair == 0 && h == 0) put_stats(a, row, qh, m, l);
@@ -660,7 +664,7 @@ hipError_t go(const AttendArgs &a, hipStream_t st) {
         launch_rows<D, false>(a, st);
     if (hipError_t e = hipGetLastError()) return e;
     // (no tile that the table allows is worth cutting)
-    if (kManyFixed + (int64_t)a.table_cols * a.cache.page <= kManyWhole) return hipSuccess;
+    if ((int64_t)a.table_cols * a.cache.page <= kManyWhole) return hipSuccess;
     attend_join_kernel<D><<<dim3(kJoinGroups), dim3(kThreads), 0, st>>>(a);
     return hipGetLastError();
 }
