@@ -1,7 +1,7 @@
 """One decode step of a multi-tenant server's last layer, as an example of how
 the serving-step operators run together:
 
-    python -m tenant_lora_serving_amd.decode_step [--rows 256] [--adapters 32]
+    python -m tenant_lora_serving_amd.decode_step [--rows 256] [--adapters 32] [--context 1000] [--prefix 0]
 
     s  = x + residual, q8 = norm(s) in e4m3        rms_norm
     qkv = q8 Wqkv^T + adapters                     lora_linear, 8-bit form
@@ -10,8 +10,9 @@ the serving-step operators run together:
     z  = h Whead^T + adapters                      lora_linear
     log probabilities of the answered tokens       token_logprobs
 
-The attention itself is the caller's (`attend`; by default the query columns
-pass through).  Workspaces are made once and used by every step, and a step
+The attention is `attend`: by default the query columns pass through;
+CachedAttention (with --context) keeps every request's keys and values in a
+paged cache (kv_append, paged_attention).  Workspaces are made once and used by every step, and a step
 allocates nothing that a graph capture cannot hold, so the example captures it
 and replays the graph; it prints the time of a step both ways.
 """
@@ -54,6 +55,66 @@ def make_projection(g, k, sizes, slots, rank, quant=False) -> Projection:
         w = w.bfloat16()
     return Projection(w, w_scale, normal(slots, len(sizes), rank, k, std=k ** -0.5).bfloat16(),
                       normal(slots, sum(sizes), rank, std=rank ** -0.5).bfloat16(), tuple(sizes))
+
+
+class CachedAttention:
+    """`attend` of a step for up to `rows` requests of up to `context` tokens each, over a paged
+    cache: appends every request's new token and attends over all of its tokens and, before
+    them, those of the prefix that it shares: request i has prefix i * len(prefixes) // rows.
+    `lens`, the tokens that each request has in the cache, lives on the device and grows by one
+    a call, in a replayed graph too; a full request's last token is written over."""
+
+    def __init__(self, heads, kv_heads, dim, rows, context, prefixes=(), page=16, quant=False, base=500000.0,
+                 device="cuda"):
+        def ints(v):
+            return torch.tensor(v, dtype=torch.int32, device=device)
+
+        self.heads, self.kv, self.dim, self.page, self.context = heads, kv_heads, dim, page, context
+        each, counts = -(-context // page), [-(-p // page) for p in prefixes]
+        shape = (2, rows * each + sum(counts), page, kv_heads, dim)
+        self.cache = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        self.scales = {}
+        if quant:
+            self.cache = self.cache.to(torch.float8_e4m3fn)
+            self.scales = {name: torch.full((kv_heads,), 1 / 64, device=device) for name in ("k_scale", "v_scale")}
+        self.pages = ints(range(rows * each)).view(rows, each)
+        self.lens = torch.zeros(rows, dtype=torch.int32, device=device)
+        self.before = torch.zeros(rows, dtype=torch.int32, device=device)
+        self.prefix = None
+        if prefixes:
+            firsts = [rows * each + sum(counts[:i]) for i in range(len(counts))]
+            tables = [[f + j if j < c else -1 for j in range(max(counts))] for f, c in zip(firsts, counts)]
+            starts = [-(-rows * i // len(prefixes)) for i in range(len(prefixes) + 1)]
+            self.prefix = step.Prefixes(ints(tables), ints(list(prefixes)), ints(starts))
+            self.before = ints([prefixes[i * len(prefixes) // rows] for i in range(rows)])
+        self.rotation = step.rotation_table(context + max(prefixes, default=0), dim, base, device)
+        self.ws = step.attention_workspace(rows, heads, kv_heads, dim, bool(prefixes), device)
+
+    def parts(self, qkv):
+        """q, k and v of a projection's result, [n, heads, dim] each."""
+        wide = [h * self.dim for h in (self.heads, self.kv, self.kv)]
+        return [p.unflatten(1, (-1, self.dim)) for p in qkv.split(wide, dim=1)]
+
+    def fill_prefix(self, i, qkv):
+        """The keys and values of prefix i's tokens, from their projection's result."""
+        _, k, v = self.parts(qkv)
+        t = torch.arange(k.shape[0], device=k.device)
+        place = self.prefix.pages[i][t // self.page] * self.page + t % self.page
+        step.kv_append(k, v, *self.cache, place.int(), positions=t.int(), rotation=self.rotation, **self.scales)
+
+    def __call__(self, qkv):
+        n = qkv.shape[0]
+        q, k, v = self.parts(qkv)
+        at = self.lens[:n].clamp_max(self.context - 1)
+        place = self.pages[:n].gather(1, (at // self.page)[:, None].long())[:, 0] * self.page + at % self.page
+        q = step.kv_append(k, v, *self.cache, place, q=q, positions=at + self.before[:n], rotation=self.rotation,
+                           **self.scales)
+        self.lens[:n] = at + 1
+        prefix = self.prefix
+        if prefix is not None and n < self.lens.shape[0]:   # (the batch is a part of the rows)
+            prefix = prefix._replace(starts=prefix.starts.clamp_max(n))
+        r = step.paged_attention(q, *self.cache, self.pages[:n], self.lens[:n], prefix=prefix, ws=self.ws, **self.scales)
+        return r.out.flatten(1)
 
 
 class StepResult(NamedTuple):
@@ -102,10 +163,17 @@ def main():
     ap.add_argument("--rows", type=int, default=256)
     ap.add_argument("--adapters", type=int, default=32)
     ap.add_argument("--rank", type=int, default=16)
+    ap.add_argument("--context", type=int, default=0, help="tokens of a request in the cache at most; 0: no attention")
+    ap.add_argument("--prefix", type=int, default=0, help="tokens of a prefix that all requests share")
     args = ap.parse_args()
     n = args.rows
     g = torch.Generator(device="cuda").manual_seed(1)
-    run = DecodeStep(4096, 1024, 128256, args.adapters, args.rank, n)
+    attend = None
+    if args.context > 0:
+        attend = CachedAttention(32, 8, 128, n, args.context, (args.prefix,) if args.prefix > 0 else ())
+        attend.cache.normal_(generator=g)
+        attend.lens.copy_(torch.randint(0, args.context, (n,), generator=g, device="cuda"))
+    run = DecodeStep(4096, 1024, 128256, args.adapters, args.rank, n, attend=attend)
     x, residual = (torch.randn(n, 4096, generator=g, device="cuda").bfloat16() for _ in range(2))
     slot = torch.randint(0, args.adapters, (n,), generator=g, device="cuda").to(torch.int32)
     tokens = torch.randint(0, 128256, (n,), generator=g, device="cuda").to(torch.int32)
