@@ -216,7 +216,7 @@ size_t step_paged_attention_workspace_bytes(int32_t n, int32_t heads, int32_t kv
  * and by nothing else.
  * Limits: n <= STEP_MAX_TOKENS; requests, prefixes <= STEP_MAX_REQUESTS;
  * table_cols * page and prefix_cols * page <= 1 << 24; leading dimensions of q
- * and out multiples of 8; q, out and ws 16-byte aligned; scale > 0 and finite.
+ * and out multiples of 8; q, out and ws 16-byte aligned; scale in [1e-30, 1e30].
  */
 int step_paged_attention(const uint16_t *q, int64_t ldq, int32_t n, int32_t requests, int32_t heads, int32_t kv_heads,
                          int32_t dim, const void *k_cache, const void *v_cache, int64_t page_stride,

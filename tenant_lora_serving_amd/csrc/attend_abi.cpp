@@ -3,8 +3,6 @@
 // synchronizes; every check runs before any launch.
 #include <hip/hip_runtime.h>
 
-#include <cmath>
-
 #include "../../include/step.h"
 #include "attend_kernels.h"
 
@@ -134,7 +132,7 @@ int step_paged_attention(const uint16_t *q, int64_t ldq, int32_t n, int32_t requ
     st::CacheArgs c{const_cast<void *>(k_cache), const_cast<void *>(v_cache), page_stride, token_stride, head_stride,
                     pages, page, k_scale, v_scale};
     if (int rc = check_cache(c, kv_heads, dim)) return rc;
-    if (!(scale > 0.0f) || std::isinf(scale)) return STEP_EINVAL;
+    if (!(scale >= 1e-30f && scale <= 1e30f)) return STEP_EINVAL;
     if (table_cols < 0 || ld_table < table_cols || prefixes < 0) return STEP_EINVAL;
     if ((int64_t)table_cols * page > kMostKeys || ld_table >= kMostStride) return STEP_EUNSUPPORTED;
     if (prefixes > 0) {

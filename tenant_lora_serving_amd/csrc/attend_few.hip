@@ -201,13 +201,15 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void attend
                 if (ok != ~0u && !((ok >> key) & 1)) vr[u] = tl::zero4();
                 char *const ks = lk + key * Sh::kK, *const vs = lv + key * Sh::kV;
                 if constexpr (F8) {
-                    // (of V, odd rows' second half first: a write's 16 bytes then fall on all banks)
-                    const bool odd = lr & 1;
-                    const int at = lc * 32 + (odd ? 16 : 0), other = lc * 32 + (odd ? 0 : 16);
-                    tl::st16(ks + lc * 32, widen8(kr[u].x, kr[u].y));
-                    tl::st16(ks + lc * 32 + 16, widen8(kr[u].z, kr[u].w));
-                    tl::st16(vs + at, widen8(odd ? vr[u].z : vr[u].x, odd ? vr[u].w : vr[u].y));
-                    tl::st16(vs + other, widen8(odd ? vr[u].x : vr[u].z, odd ? vr[u].y : vr[u].w));
+                    // (some lanes' second half first, so that 8 lanes' 16 bytes fall on different banks)
+                    const bool swap_v = lane & 4, swap_k = swap_v && D > 64;
+                    auto put = [&](char *to, const u32x4_t x, bool swap) {
+                        const int first = lc * 32 + (swap ? 16 : 0), second = lc * 32 + (swap ? 0 : 16);
+                        tl::st16(to + first, widen8(swap ? x.z : x.x, swap ? x.w : x.y));
+                        tl::st16(to + second, widen8(swap ? x.x : x.z, swap ? x.y : x.w));
+                    };
+                    put(ks, kr[u], swap_k);
+                    put(vs, vr[u], swap_v);
                 } else {
                     tl::st16(ks + lc * 16, kr[u]);
                     tl::st16(vs + lc * 16, vr[u]);

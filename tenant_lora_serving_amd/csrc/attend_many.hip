@@ -117,7 +117,7 @@ __device__ __forceinline__ float2 *piece_stats(const AttendArgs &a, int slot, in
 }
 
 // Even: pages hold whole groups of the keys that a load instruction takes, so
-// that places are worked out once a wave, with scalar instructions.
+// that a place is worked out for each group, not by every lane for its key.
 template <int D, bool F8>
 constexpr int kKeysOfLoad = kWave * 16 / (D * (F8 ? 1 : 2));
 template <int D, bool F8, bool Even>

@@ -111,7 +111,8 @@ def test_attention_refusals(L):
     for bad in CACHE_REFUSED + [
             dict(q=0), dict(q=0x10008), dict(ldq=504), dict(ldq=516), dict(requests=4), dict(requests=-1, starts=0x6000),
             dict(starts=0x6000, max_rows=0), dict(starts=0x6002), dict(table=0), dict(table=2), dict(ldt=7), dict(cols=-1),
-            dict(lens=0), dict(lens=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf),
+            dict(lens=0), dict(lens=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(scale=1e-31),
+            dict(scale=1e31),
             dict(out=0), dict(out=0x90008), dict(ldo=504), dict(ldo=516), dict(lse=2), dict(prefixes=-1),
             dict(PREFIXED, pt=0), dict(PREFIXED, ldp=5), dict(PREFIXED, pl=0), dict(PREFIXED, pst=0),
             dict(PREFIXED, pcols=-1)]:
@@ -158,6 +159,21 @@ def test_which_kernels(L):
     L.stub_reset()
     attend(L, n=1, requests=1)
     assert 1 <= launches(L)[0][1] <= 8
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    from tenant_lora_serving_amd import step
+    x, cache = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 16, 4, 64, dtype=torch.bfloat16)
+    at = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        step.kv_append(x, x, cache, cache, at)
+    with pytest.raises(TypeError):
+        step.paged_attention(x, cache, cache, torch.zeros(2, 1, dtype=torch.int32), at)
+    with pytest.raises(ValueError):
+        step.rotation_table(10, 0, device="cpu")
+    t = step.rotation_table(4, 2, device="cpu")
+    assert t.dtype == torch.float32 and t.tolist() == [[pytest.approx(math.cos(i)), pytest.approx(math.sin(i))] for i in range(4)]
 
 
 # ---------------------------------------------------------------- pages
