@@ -8,7 +8,10 @@
 // in one pass over the keys with the running maximum m and sum.  Bound by the
 // matrix cores, the exponentials and LDS reads.  Each of the four waves holds 32
 // rows; all read the keys and values from LDS, two buffers in turn, the next 64
-// keys on their way meanwhile, one barrier a round.
+// keys on their way meanwhile, one barrier a round.  2048 rows of 4 requests over
+// 4000 to 24000 keys, 32 heads of 128: 711 us in all, 0.8 PFLOP/s, matrix
+// instructions busy 48% of the cycles; whole prompts of 6947 rows: 145 us, of
+// which 14 join pieces.
 //
 // S^T = K Q^T gives a lane one row of q and half of the keys, and p as it lies
 // there is the operand that O^T = V^T P^T wants, with the keys of the product

@@ -166,6 +166,15 @@ def test_two_tokens_with_one_place():
         assert (c == 0).all()
 
 
+def test_a_cache_past_32_bits():
+    far = torch.zeros(2 ** 31 + 2 ** 20, dtype=torch.bfloat16, device="cuda")
+    kc, vc = (far.as_strided((3, 4, 2, 64), (2 ** 30, 128, 64, 1), at) for at in (0, 4096))
+    x = torch.randn(2, 2, 64, generator=gen(4), device="cuda").bfloat16()
+    step.kv_append(x, -x, kc, vc, torch.tensor([11, 6], dtype=torch.int32, device="cuda"))
+    for c, y in ((kc, x), (vc, -x)):
+        assert torch.equal(c[2, 3], y[0]) and torch.equal(c[1, 2], y[1])
+
+
 def test_the_table():
     t = step.rotation_table(131072, 64, 5e5)
     assert t.shape == (131072, 64) and t.dtype == torch.float32

@@ -413,9 +413,10 @@ def test_graph_follows_lengths_and_tables():
             assert torch.equal(held.out, again.out) and torch.equal(held.lse, again.lse)
 
 
-def test_a_cache_past_32_bits():
+@pytest.mark.parametrize("decode", [True, False])
+def test_a_cache_past_32_bits(decode):
     """Pages that begin past 2^31 elements and past 2^32 bytes."""
-    b = Batch(60, [1, 1], [100, 40], heads=2, kv=1, decode=True)
+    b = Batch(60, [1, 1] if decode else [30, 7], [100, 40], heads=2, kv=1, decode=decode)
     far = torch.empty(2 ** 31 + 2 ** 24, dtype=torch.bfloat16, device="cuda")
     total = b.k_cache.shape[0]
     stride = (2 ** 31) // (total - 1) // 8 * 8
