@@ -431,7 +431,7 @@ def _table(t: torch.Tensor, name: str, rows: int, dev: int) -> tuple:
         raise ValueError(f"{name} is on another device")
     cols = t.shape[1]
     _fits("step_paged_attention", cols)
-    return p, max(ld, cols), cols
+    return p, ld, cols   # (rows that overlap, as an expanded table's do, are refused by the library)
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, pages: torch.Tensor,
@@ -441,12 +441,12 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
                     stream=None) -> AttentionResult:
     """Attention of the rows q [n, heads, dim] bf16 over the paged cache.  Request b reads lens[b]
-    keys (int32) on the pages pages[b] (int32 page numbers) for its row b or, with starts
-    ([requests + 1] int32, ascending), its rows starts[b] .. starts[b + 1], at most max_rows of
-    them (which only decides how the work is cut).  causal: a request's rows are its last
-    tokens and see no later key.  prefix: keys that groups of requests share and see before
-    their own.  scale: dim ** -0.5 by default.  A row without keys is 0.  Rows of no request
-    stay as they are in `out`, and are not written in a new result."""
+    keys (int32) on the pages pages[b] (int32 page numbers; rows of the table do not overlap) for
+    its row b or, with starts ([requests + 1] int32, ascending), its rows starts[b] ..
+    starts[b + 1], at most max_rows of them (which only decides how the work is cut).  causal: a
+    request's rows are its last tokens and see no later key.  prefix: keys that groups of
+    requests share and see before their own.  scale: dim ** -0.5 by default.  A row without keys
+    is 0.  Rows of no request stay as they are in `out`, and are not written in a new result."""
     if stream is not None:
         return _on(stream, paged_attention, (q, k_cache, v_cache, pages, lens),
                    dict(starts=starts, max_rows=max_rows, scale=scale, causal=causal, prefix=prefix, k_scale=k_scale,
