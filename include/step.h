@@ -170,7 +170,7 @@ int step_token_logprobs(const void *logits, int64_t ld, int32_t fp32, int32_t n,
  *    place  [n]; a token whose place is not in the cache is not stored
  *    q_out  [n][ldo]; may be q itself (then ldo == ldq)
  * In e4m3 a value over its head's scale is rounded to nearest, and to +-448 where
- * it is larger.  A position outside the rotation makes the token's q NaN, and the
+ * it is larger; over a scale of 0 a 0 is stored as 0, any other as +-448.  A position outside the rotation makes the token's q NaN, and the
  * token is not stored.  Where two tokens have one place, each 16 values (8 in
  * bf16) of it are one of the two's.  Limits: n <= STEP_MAX_TOKENS; rot a multiple
  * of 16, at most dim; leading dimensions multiples of 8; q, k, v, q_out and

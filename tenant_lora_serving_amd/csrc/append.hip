@@ -34,11 +34,12 @@ __device__ __forceinline__ float saturate(float v) {
 }
 // Eight values over a scale as e4m3, round to nearest even.  (Divided, not
 // multiplied by 1 / scale: that rounds twice and moves values across the border
-// between two neighbours.)
+// between two neighbours.  A 0 over a scale of 0, that of a head which held only
+// zeros, stays a 0.)
 __device__ __forceinline__ uint2 pack8_e4m3(const float *f, float scale) {
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = saturate(f[i] / scale);
+    for (int i = 0; i < 8; ++i) v[i] = f[i] == 0.0f && scale == 0.0f ? f[i] : saturate(f[i] / scale);
     int a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
     a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], a, true);
     int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);

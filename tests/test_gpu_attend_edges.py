@@ -23,3 +23,47 @@ def test_tables_whose_rows_overlap_are_refused():
     # the same pages for every request, a row of memory each
     b.pages = b.pages[:1].repeat(4, 1)
     check(b, "one table")
+
+
+# ---------------------------------------------------------------- scales of 0 and NaN
+def test_values_over_a_scale_of_0():
+    """A 0 is stored as 0; other values over a scale of 0 are larger than 448 and stored as that; NaN stays."""
+    x = torch.zeros(1, 2, 16, device="cuda", dtype=torch.bfloat16)
+    x[0, :, :7] = torch.tensor([0.0, -0.0, 1.0, -1e-38, math.inf, -math.inf, math.nan], device="cuda")
+    kc, vc = (torch.ones(1, 1, 2, 16, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    scale = torch.tensor([0.0, 1.0], device="cuda")
+    step.kv_append(x, x, kc, vc, ints([0]), k_scale=scale, v_scale=scale)
+    for c in (kc, vc):
+        got = c.float()[0, 0]
+        assert got[0, :6].tolist() == [0.0, 0.0, 448.0, -448.0, 448.0, -448.0] and math.isnan(got[0, 6].item())
+        assert (got[0, 7:] == 0).all()
+        assert got[1, :6].tolist() == [0.0, 0.0, 1.0, 0.0, 448.0, -448.0] and math.isnan(got[1, 6].item())
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("zero", ["head of zeros", "head of values"])
+@pytest.mark.parametrize("neighbours", [False, True])
+def test_append_and_attend_with_a_scale_of_0(rows, zero, neighbours):
+    """A head whose scale is 0 counts as zeros: its keys score 0, its values are 0."""
+    n, kv, dim = 40, 2, 64
+    g = gen(71)
+    k, v = (torch.randn(n, kv, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn(rows, 4, dim, generator=g, device="cuda").bfloat16()
+    if zero == "head of zeros":
+        k[:, 0], v[:, 1] = 0, 0
+    kc, vc = (torch.zeros(3, 16, kv, dim, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    scales = dict(k_scale=torch.tensor([0.0, 0.01], device="cuda"), v_scale=torch.tensor([0.01, 0.0], device="cuda"))
+    t = torch.arange(n, dtype=torch.int32, device="cuda")
+    step.kv_append(k, v, kc, vc, t, positions=t, rotation=step.rotation_table(n, dim), neighbours=neighbours, **scales)
+    assert torch.isfinite(kc.float()).all() and torch.isfinite(vc.float()).all()
+    r = step.paged_attention(q, kc, vc, ints([[0, 1, 2]]), ints([n]), starts=ints([0, rows]), max_rows=rows, causal=False,
+                             lse=True, **scales)
+    # the mean of the values in the cache: terms of p = 1, which bf16 holds, fp32 sums, one rounding
+    held = vc.double().flatten(0, 1)[:n, 0] * scales["v_scale"][0].double()
+    want, tol = held.mean(dim=0), held.mean(dim=0).abs() * 2.0 ** -8 + held.abs().sum(dim=0) * 2.0 ** -20
+    near(r.out[:, :2], want.expand(rows, 2, dim), tol.expand(rows, 2, dim), "keys of scale 0")
+    assert (r.out[:, 2:] == 0).all()
+    # (p = 1 exactly: ln 40 from log2 and its product with ln 2)
+    near(r.lse[:, :2], torch.full((rows, 2), math.log(n), dtype=torch.float64, device="cuda"),
+         torch.full((rows, 2), 2.0 ** -20, dtype=torch.float64, device="cuda"), "lse")
+    assert torch.isfinite(r.lse).all()
