@@ -145,7 +145,7 @@ struct PageDiv {
 };
 __host__ __device__ inline PageDiv page_div(int page) {
     int up = 0;
-    while ((1 << up) < page) ++up;
+    while (1ll << up < page) ++up;  // (64 bits: a page may hold more than 2^30)
     return {(uint32_t)((1ull << (24 + up)) / page + 1), 24 + up};
 }
 __host__ __device__ inline int page_of(PageDiv d, int key) { return (int)(((uint64_t)(uint32_t)key * d.mul) >> d.shift); }
