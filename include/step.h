@@ -208,12 +208,12 @@ size_t step_paged_attention_workspace_bytes(int32_t n, int32_t heads, int32_t kv
  *    starts [requests + 1] and prefix_starts [prefixes + 1] ascending
  *    max_rows   the most rows of a request; it decides only which kernel runs
  * Rows that belong to no request stay as they are.  A row without keys gets 0
- * and lse -infinity.  Keys on a page number that the cache does not have count as
- * absent, lengths end with the table.  Keys whose score is -infinity are absent
- * too; an infinity or NaN reaches no row that does not see its key.  Products in
- * bf16 with fp32 sums, p rounded to bf16 before its product with v, one rounding
- * of the result; the order of the sums goes by the lengths of the whole batch,
- * and by nothing else.
+ * and lse -infinity; one that sees keys whose scale is NaN or infinite gets NaN.
+ * Keys on a page number that the cache does not have count as absent, lengths end
+ * with the table.  Keys whose score is -infinity are absent too; an infinity or
+ * NaN reaches no row that does not see its key.  Products in bf16 with fp32 sums,
+ * p rounded to bf16 before its product with v, one rounding of the result; the
+ * order of the sums goes by the lengths of the whole batch, and by nothing else.
  * Limits: n <= STEP_MAX_TOKENS; requests, prefixes <= STEP_MAX_REQUESTS;
  * table_cols * page and prefix_cols * page <= 1 << 24; leading dimensions of q
  * and out multiples of 8; q, out and ws 16-byte aligned; scale in [1e-30, 1e30].

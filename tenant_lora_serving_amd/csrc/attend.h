@@ -222,6 +222,29 @@ __device__ __forceinline__ uint64_t token_offset(const AttendArgs &a, int page, 
     return ((uint64_t)(uint32_t)page * a.page_units + (uint64_t)(uint32_t)in_page * a.token_units) * 16;
 }
 
+// ---------------------------------------------------------------- scales of a head
+// What turns scores into exponents.  A scale of 0, of a head that is all zeros,
+// must not meet the masks' infinity; one that is not finite is left out, and the
+// rows that see such keys become NaN when they are finished.
+__device__ __forceinline__ float scale_of_scores(const AttendArgs &a, int g) {
+    return a.scale * (a.cache.k_scale ? a.cache.k_scale[g] : 1.0f);
+}
+__device__ __forceinline__ float exponent_factor(const AttendArgs &a, int g) {
+    const float c = scale_of_scores(a, g);
+    return c < INFINITY ? fmaxf(c, 1e-30f) : 1.0f;
+}
+// What a row's weighted sum of values is multiplied by, and the logarithm of its sum.
+struct Finish {
+    bool finite;
+    float values;
+    __device__ __forceinline__ Finish(const AttendArgs &a, int g)
+        : finite(scale_of_scores(a, g) < INFINITY), values(a.cache.v_scale ? a.cache.v_scale[g] : 1.0f) {}
+    __device__ __forceinline__ float factor(float l) const { return l == 0.0f ? 0.0f : finite ? values / l : NAN; }
+    __device__ __forceinline__ float log_sum(float m, float l) const {
+        return l == 0.0f ? -INFINITY : finite ? (base_of(m) + log2f(l)) * kLn2 : NAN;
+    }
+};
+
 // ---------------------------------------------------------------- results of pieces
 // Words that another workgroup, perhaps on another XCD, reads: written through
 // to memory and read from there.

@@ -46,7 +46,7 @@ template <int D>
 __device__ __forceinline__ void few_results(const AttendArgs &a, const Walk &w, const TileRows &t, const Piece &p,
                                             const FewShared<D> &sh, bool whole) {
     using Sh = FewShared<D>;
-    const float vs = a.cache.v_scale ? a.cache.v_scale[w.g] : 1.0f;
+    const Finish finish(a, w.g);
     for (int e = threadIdx.x; e < t.count * (D / 4); e += kThreads) {
         const int r = e / (D / 4), c = e % (D / 4) * 4;
         float m = -INFINITY, l = 0.0f;
@@ -72,11 +72,11 @@ __device__ __forceinline__ void few_results(const AttendArgs &a, const Walk &w, 
             *reinterpret_cast<f32x4_t *>(a.sums_out + rh * D + c) = o;
             continue;
         }
-        const float f = l == 0.0f ? 0.0f : vs / l;
+        const float f = finish.factor(l);
         if (c < a.dim)
             *reinterpret_cast<uint2 *>(a.out + row * a.ldo + head * a.dim + c) =
                 make_uint2(tl::pack_bf16x2(o[0] * f, o[1] * f), tl::pack_bf16x2(o[2] * f, o[3] * f));
-        if (c == 0 && a.lse) a.lse[rh] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
+        if (c == 0 && a.lse) a.lse[rh] = finish.log_sum(m, l);
     }
 }
 
@@ -152,8 +152,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : D > 64 ? 2 : 3) void attend
             const int c = 32 * kk + 8 * h;
             q[kk] = live && c < a.dim ? tl::ld16(a.q + row * a.ldq + qh * a.dim + c) : tl::zero4();
         }
-        // (a scale of 0, of a head that is all zeros, must not meet the masks' infinity)
-        const float cf = fmaxf(a.scale * (F8 ? a.cache.k_scale[w.g] : 1.0f), 1e-30f);
+        const float cf = exponent_factor(a, w.g);
         float m = -INFINITY, l = 0.0f;
         f32x4_t acc[D / 16] = {};
         if (a.state_in && wave == 0 && p.begins && live) {

@@ -96,15 +96,12 @@ __device__ __forceinline__ void put_columns(const AttendArgs &a, int64_t row, in
         *reinterpret_cast<uint2 *>(a.out + row * a.ldo + qh * a.dim + c) =
             make_uint2(tl::pack_bf16x2(o[0] * f, o[1] * f), tl::pack_bf16x2(o[2] * f, o[3] * f));
 }
-__device__ __forceinline__ void put_stats(const AttendArgs &a, int64_t row, int qh, float m, float l) {
+__device__ __forceinline__ void put_stats(const AttendArgs &a, int64_t row, int qh, const Finish &finish, float m, float l) {
     const int64_t rh = row * (a.kv * a.each) + qh;
     if (a.state_out)
         *reinterpret_cast<float2 *>(a.state_out + 2 * rh) = make_float2(m, l);
     else if (a.lse)
-        a.lse[rh] = l == 0.0f ? -INFINITY : (base_of(m) + log2f(l)) * kLn2;
-}
-__device__ __forceinline__ float result_factor(const AttendArgs &a, int g, float l) {
-    return l == 0.0f ? 0.0f : (a.cache.v_scale ? a.cache.v_scale[g] : 1.0f) / l;
+        a.lse[rh] = finish.log_sum(m, l);
 }
 
 // Pieces' results lie as the lanes hold them: pair i of a lane's columns, then the rows' maxima and sums.
@@ -163,8 +160,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
             const int c = 16 * kk + 8 * h;
             q[kk] = live && c < a.dim ? tl::ld16(a.q + row * a.ldq + qh * a.dim + c) : tl::zero4();
         }
-        // (a scale of 0, of a head that is all zeros, must not meet the masks' infinity)
-        const float cf = fmaxf(a.scale * (F8 ? a.cache.k_scale[w.g] : 1.0f), 1e-30f);
+        const float cf = exponent_factor(a, w.g);
         RowState<D> x;
         // The piece's keys.  The quick way leaves out two things that hardly ever
         // happen, keys on pages that the cache does not have and, among the values of
@@ -561,14 +557,15 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attend_many_kernel(
         }
         if (!p.split) {
             if (live) {
-                const float f = result_factor(a, w.g, x.l);
+                const Finish finish(a, w.g);
+                const float f = finish.factor(x.l);
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         put_columns(a, row, qh, D, 32 * j + 8 * i + 4 * h, f,
                                     f32x4_t{x.o[j][4 * i], x.o[j][4 * i + 1], x.o[j][4 * i + 2], x.o[j][4 * i + 3]});
-                if (h == 0) put_stats(a, row, qh, x.m, x.l);
+                if (h == 0) put_stats(a, row, qh, finish, x.m, x.l);
             }
         } else {
             if (any) {
@@ -641,12 +638,13 @@ __global__ __launch_bounds__(kThreads) void attend_join_kernel(AttendArgs a) {
         if (r >= t.rows) continue;
         const int64_t row = t.row + r / a.each;
         const int qh = t.g * a.each + r % a.each;
-        const float f = result_factor(a, t.g, l);
+        const Finish finish(a, t.g);
+        const float f = finish.factor(l);
 #pragma unroll
         for (int i = 0; i < kPairs; i += 2)  // (four columns)
             put_columns(a, row, qh, D, 32 * ((pair + i) / 8) + 8 * ((pair + i) % 8 / 2) + 4 * h, f,
                         f32x4_t{o[i].x, o[i].y, o[i + 1].x, o[i + 1].y});
-        if (pair == 0 && h == 0) put_stats(a, row, qh, m, l);
+        if (pair == 0 && h == 0) put_stats(a, row, qh, finish, m, l);
     }
 }
 

@@ -1,5 +1,5 @@
-"""Calls of the paged cache's operators at the edge of what they accept: refusals, scales of 0 and NaN, and the
-second, careful way of the many-row kernel in every form.  Definition and bounds are those of test_gpu_attend.py."""
+"""Calls of the paged cache's operators at the edge of what they accept: refusals, scales of 0 and not finite, and
+the second, careful way of the many-row kernel in every form.  Definition and bounds are those of test_gpu_attend.py."""
 import math
 
 import pytest
@@ -25,7 +25,7 @@ def test_tables_whose_rows_overlap_are_refused():
     check(b, "one table")
 
 
-# ---------------------------------------------------------------- scales of 0 and NaN
+# ---------------------------------------------------------------- scales of 0, infinite and NaN
 def test_values_over_a_scale_of_0():
     """A 0 is stored as 0; other values over a scale of 0 are larger than 448 and stored as that; NaN stays."""
     x = torch.zeros(1, 2, 16, device="cuda", dtype=torch.bfloat16)
@@ -67,3 +67,19 @@ def test_append_and_attend_with_a_scale_of_0(rows, zero, neighbours):
     near(r.lse[:, :2], torch.full((rows, 2), math.log(n), dtype=torch.float64, device="cuda"),
          torch.full((rows, 2), 2.0 ** -20, dtype=torch.float64, device="cuda"), "lse")
     assert torch.isfinite(r.lse).all()
+
+
+@pytest.mark.parametrize("rows,lens,prefixes", [
+    ([1] * 5, [0, 40, 3000, 1, 300], ()), ([3, 2, 9, 1], [40, 0, 20, 1000], ()), ([40, 130, 7, 300], [300, 50, 0, 4000], ()),
+    ([1] * 9, [0, 40, 0, 5, 70, 0, 9, 300, 1], ((50, 3), (0, 2))), ([20, 3, 50], [0, 300, 20], ((900, 2),))])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_a_scale_of_the_keys_that_is_not_finite(rows, lens, prefixes, value):
+    """It reaches every row of its head that sees a key, and no other."""
+    decode = max(rows) == 1
+    b = Batch(72, rows, lens, cache="e4m3", prefixes=prefixes, first=0, decode=decode)
+    out, lse, tol, tol_lse = b.want()
+    b.k_scale[1] = value
+    seen = torch.isfinite(lse[:, 4:])
+    out[:, 4:][seen], lse[:, 4:][seen] = math.nan, math.nan
+    assert seen.any() and not seen.all()
+    check(b, f"scale {value}", want=(out, lse, tol, tol_lse))
