@@ -69,7 +69,10 @@ class CachedAttention:
         def ints(v):
             return torch.tensor(v, dtype=torch.int32, device=device)
 
+        if context < 1 or page < 1 or min(prefixes, default=0) < 0:
+            raise ValueError("context and page must be at least 1, prefixes at least 0 tokens long")
         self.heads, self.kv, self.dim, self.page, self.context = heads, kv_heads, dim, page, context
+        self.prefixes = tuple(prefixes)
         each, counts = -(-context // page), [-(-p // page) for p in prefixes]
         shape = (2, rows * each + sum(counts), page, kv_heads, dim)
         self.cache = torch.zeros(shape, dtype=torch.bfloat16, device=device)
@@ -105,7 +108,7 @@ class CachedAttention:
     def __call__(self, qkv):
         n = qkv.shape[0]
         q, k, v = self.parts(qkv)
-        at = self.lens[:n].clamp_max(self.context - 1)
+        at = self.lens[:n].clamp(0, self.context - 1)
         place = self.pages[:n].gather(1, (at // self.page)[:, None].long())[:, 0] * self.page + at % self.page
         q = step.kv_append(k, v, *self.cache, place, q=q, positions=at + self.before[:n], rotation=self.rotation,
                            **self.scales)

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from tenant_lora_serving_amd import step
+from tenant_lora_serving_amd.decode_step import CachedAttention
 from tenant_lora_serving_amd.lora import LoraError
 from test_gpu_attend import Batch, check, gen, ints, near
 
@@ -83,3 +84,17 @@ def test_a_scale_of_the_keys_that_is_not_finite(rows, lens, prefixes, value):
     out[:, 4:][seen], lse[:, 4:][seen] = math.nan, math.nan
     assert seen.any() and not seen.all()
     check(b, f"scale {value}", want=(out, lse, tol, tol_lse))
+
+
+# ---------------------------------------------------------------- the cached attention of a decode step
+def test_lengths_that_lie_outside_the_cache():
+    """A negative length counts as 0, one past the context as a full request: its last token is written over."""
+    g = gen(73)
+    a = CachedAttention(4, 2, 64, 3, 20)
+    a.lens.copy_(ints([-5, 2 ** 31 - 1, -2 ** 31]))
+    qkv = torch.randn(3, 8 * 64, generator=g, device="cuda").bfloat16()
+    out = a(qkv).view(3, 4, 64)
+    assert a.lens.tolist() == [1, 20, 1]
+    v = a.parts(qkv)[2].repeat_interleave(2, dim=1)
+    assert torch.equal(out[0], v[0]) and torch.equal(out[2], v[2])     # (a first token's own value)
+    assert torch.isfinite(out[1]).all()
