@@ -99,7 +99,11 @@ class CachedAttention:
         return [p.unflatten(1, (-1, self.dim)) for p in qkv.split(wide, dim=1)]
 
     def fill_prefix(self, i, qkv):
-        """The keys and values of prefix i's tokens, from their projection's result."""
+        """The keys and values of all of prefix i's tokens, from their projection's result."""
+        if not 0 <= i < len(self.prefixes):
+            raise IndexError(f"there is no prefix {i}")
+        if qkv.shape[0] != self.prefixes[i]:
+            raise ValueError(f"prefix {i} has {self.prefixes[i]} tokens, got {qkv.shape[0]}")
         _, k, v = self.parts(qkv)
         t = torch.arange(k.shape[0], device=k.device)
         place = self.prefix.pages[i][t // self.page] * self.page + t % self.page
