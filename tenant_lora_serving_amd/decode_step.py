@@ -173,11 +173,13 @@ def main():
     ap.add_argument("--context", type=int, default=0, help="tokens of a request in the cache at most; 0: no attention")
     ap.add_argument("--prefix", type=int, default=0, help="tokens of a prefix that all requests share")
     args = ap.parse_args()
+    if args.context < 0 or args.prefix < 0 or (args.prefix > 0 and args.context == 0):
+        ap.error("--context and --prefix are lengths, and --prefix needs a --context")
     n = args.rows
     g = torch.Generator(device="cuda").manual_seed(1)
     attend = None
-    if args.context > 0:
-        attend = CachedAttention(32, 8, 128, n, args.context, (args.prefix,) if args.prefix > 0 else ())
+    if args.context:
+        attend = CachedAttention(32, 8, 128, n, args.context, (args.prefix,) if args.prefix else ())
         attend.cache.normal_(generator=g)
         attend.lens.copy_(torch.randint(0, args.context, (n,), generator=g, device="cuda"))
     run = DecodeStep(4096, 1024, 128256, args.adapters, args.rank, n, attend=attend)

@@ -1,4 +1,7 @@
 """What decode_step's CachedAttention refuses before anything is launched (no GPU)."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -32,3 +35,10 @@ def test_sizes_of_the_cache():
             make(**bad)
     a = make(prefixes=(0, 3))
     assert a.prefix.lens.tolist() == [0, 3] and a.prefix.pages.shape == (2, 1)
+
+
+def test_the_command_refuses_a_prefix_without_a_context():
+    for more in (["--prefix", "50"], ["--context", "-1"], ["--context", "9", "--prefix", "-2"]):
+        r = subprocess.run([sys.executable, "-m", "tenant_lora_serving_amd.decode_step", "--rows", "3", *more],
+                           capture_output=True, text=True, timeout=100)
+        assert r.returncode == 2 and "--" in r.stderr, r.stderr[-500:]
