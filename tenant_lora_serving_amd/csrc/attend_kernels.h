@@ -34,12 +34,13 @@ hipError_t launch_kv_append(const AppendArgs &a, hipStream_t st);
 
 // ---------------------------------------------------------------- division of the work
 // The rows of a request times the query heads that share a key head are cut
-// into tiles of `tokens` rows by `each` heads.  A tile costs kTileCost and the
-// keys that its last row sees.  All tiles' costs one after another, request by
+// into tiles of `tokens` rows by `each` heads.  A tile costs `fixed` and the keys
+// that its last row sees.  All tiles' costs one after another, request by
 // request, key head by key head, are cut into equal ranges, one for every
-// workgroup.  A tile of more than `whole` keys, or a quarter of a range, is cut where the ranges
-// meet, and its pieces' results go to the workspace and are joined; a smaller
-// one belongs to the workgroup that its middle falls to.
+// workgroup.  A tile that costs more than one of `whole` keys, and more than a
+// quarter of a range, is cut where the ranges meet, and its pieces' results go to
+// the workspace and are joined; a smaller one belongs to the workgroup that its
+// middle falls to.
 // Everything follows from the lengths, so the device divides by itself and a
 // captured call follows lengths that change.
 struct Span {

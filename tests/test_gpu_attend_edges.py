@@ -98,3 +98,69 @@ def test_lengths_that_lie_outside_the_cache():
     v = a.parts(qkv)[2].repeat_interleave(2, dim=1)
     assert torch.equal(out[0], v[0]) and torch.equal(out[2], v[2])     # (a first token's own value)
     assert torch.isfinite(out[1]).all()
+
+
+# ---------------------------------------------------------------- the careful way
+def careful_batch(seed, rows, lens, prefixes, dim, cache, page):
+    """Values that are not finite behind most of the rows, a NaN key that the last row alone sees, pages that are
+    not there among the request's own and the prefix's: nothing of it may reach a row that does not see it."""
+    b = Batch(seed, rows, lens, heads=4, kv=1, dim=dim, cache=cache, page=page, prefixes=prefixes)
+    worst = math.nan if cache == "e4m3" else math.inf
+
+    def at(table, j):
+        return table[j // page].item(), j % page
+    for request, (r, n) in enumerate(zip(rows, lens)):
+        p, t = at(b.pages[request], n - 2)
+        b.v_cache[p, t, 0, 7], b.v_cache[p, t, 0, dim - 1] = worst, math.nan
+        if request == 0:
+            p, t = at(b.pages[request], n - 1)
+            b.k_cache[p, t, 0, 5], b.v_cache[p, t, 0, 3] = math.nan, -worst
+    pages = b.pages.clone()
+    pages[1, 0] = 2 ** 31 - 1
+    if lens[0] // page // 2 < (lens[0] - 2) // page:
+        pages[0, lens[0] // page // 2] = -1
+    if prefixes:
+        p, t = at(b.prefix.pages[1], prefixes[1][0] - 1)
+        b.v_cache[p, t, 0, 9] = worst
+        b.prefix.pages[0, 1] = b.k_cache.shape[0]
+    return b, pages
+
+
+@pytest.mark.parametrize("page", [3, 16, 100])
+@pytest.mark.parametrize("dim", [64, 80, 128, 256])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,lens", [([60, 9, 130], [60, 200, 300]), ([100, 33], [9000, 3000]), ([4, 3], [40, 130]),
+                                       ([4, 2], [6000, 5000])])
+@pytest.mark.parametrize("shared", [False, True])
+def test_what_is_not_finite_reaches_no_row_before_it(page, dim, cache, rows, lens, shared):
+    prefixes = ((2500, 1), (70, len(rows) - 1)) if shared else ()
+    b, pages = careful_batch(80, rows, lens, prefixes, dim, cache, page)
+    r = check(b, f"{dim} {cache} {page}", pages=pages)
+    last = rows[0] - 1
+    assert torch.isfinite(r.out[:last - 1]).all() and torch.isnan(r.out[last]).all()
+
+
+def test_what_is_not_finite_reaches_every_row_that_sees_it():
+    """A cut tile of which one piece is done the careful way, with the same bits each time."""
+    rows, lens = [100, 33], [9000, 3000]
+    b = Batch(81, rows, lens, heads=4, kv=1)
+    b.v_cache[b.pages[0, 0].item(), 0, 0, 0] = math.inf      # (every row of request 0 sees it: its column 0 is infinite)
+    r = check(b, "seen by all")
+    assert torch.isinf(r.out[:100, :, 0]).all() and torch.isfinite(r.out[:, :, 1:]).all()
+    again = b.call()
+    assert torch.equal(r.out, again.out) and torch.equal(r.lse, again.lse)
+
+
+def test_prefix_starts_that_make_no_sense_stay_inside():
+    b = Batch(82, [1] * 9, [40] * 9, prefixes=((50, 4), (20, 3)), decode=True)
+    c = Batch(83, [30] * 9, [40] * 9, prefixes=((50, 4), (20, 3)))
+    for x in (b, c):
+        n = x.q.shape[0]
+        ws = step.attention_workspace(n, 8, 2, 128, prefixes=True)
+        out = torch.full((n + 8, 8, 128), 7.0, device="cuda", dtype=torch.bfloat16)
+        for ends in ([0, -5, 100], [9, 5, 1], [-1, -1, 2 ** 31 - 1], [2 ** 31 - 1, 0, -2 ** 31]):
+            x.call(prefix=x.prefix._replace(starts=ints(ends)), out=out[4:-4], ws=ws)
+            assert (out[:4] == 7).all() and (out[-4:] == 7).all()
+        want = x.want()
+        assert (ws[:4096] == 0).all()
+        near(x.call(out=out[4:-4], ws=ws).out, want[0], want[2], "afterwards")
