@@ -206,14 +206,19 @@ size_t step_paged_attention_workspace_bytes(int32_t n, int32_t heads, int32_t kv
  * have no prefix.  Each prefix is read once for all its requests.
  *    q [n][ldq], out [n][ldo], heads * dim used columns; lse [n][heads]
  *    starts [requests + 1] and prefix_starts [prefixes + 1] ascending
+ *    table, prefix_table  rows ld_table and ld_prefix_table apart, which do not overlap
  *    max_rows   the most rows of a request; it decides only which kernel runs
  * Rows that belong to no request stay as they are.  A row without keys gets 0
  * and lse -infinity; one that sees keys whose scale is NaN or infinite gets NaN.
  * Keys on a page number that the cache does not have count as absent, lengths end
- * with the table.  Keys whose score is -infinity are absent too; an infinity or
- * NaN reaches no row that does not see its key.  Products in bf16 with fp32 sums,
- * p rounded to bf16 before its product with v, one rounding of the result; the
- * order of the sums goes by the lengths of the whole batch, and by nothing else.
+ * with the table.  A key whose score is -infinity weighs nothing, and a row all of
+ * whose keys are such is one without keys; but an infinity or NaN among the values
+ * of a key makes that column infinite or NaN in every row that sees the key, and in
+ * no other.  Products in bf16 with fp32 sums, p rounded to bf16 before its product
+ * with v, one rounding of the result; the sums of p v have to stay within fp32 with
+ * p up to 2^8.  The same call on the same inputs gives the same bits.  Other sizes,
+ * max_rows or widths of the tables, other lengths or values of the batch may change
+ * the order of a row's sums, and so its last bits.
  * Limits: n <= STEP_MAX_TOKENS; requests, prefixes <= STEP_MAX_REQUESTS;
  * table_cols * page and prefix_cols * page <= 1 << 24; leading dimensions of q
  * and out multiples of 8; q, out and ws 16-byte aligned; scale in [1e-30, 1e30].
