@@ -127,11 +127,23 @@ constexpr int kFewRows = 16, kManyRows = 128;  // rows of a tile: of few rows, o
 constexpr int kMaxEach = 64;                   // query heads of a key head
 constexpr int kMaxDim = 256;
 constexpr int kFewGroups = 768, kManyGroups = 512;  // workgroups at most
-// What a tile costs beside its keys, in keys (about 6 us of a workgroup's time;
-// 256 requests over 64 to 4096 keys of 8 bits: 102 us, with 64 for it 135).
+// The constants of the division, each with what other values measured.  (256
+// decode: that many tokens over 64 to 4096 keys, 8 key heads of 128 where no other
+// size is named; us a call.)
+// What a tile costs beside its keys, in keys, some 6 us of a workgroup's time.
+// Few: 256 decode 175, with 64 for it 192, with 320 181; 4 heads of 256 192, 213
+// and 180.  Few of 8 bits: 99, with 128 120, with 512 105; heads of 64 94, 100 and
+// 96; of 256 139, 151 and 151.  Many: prompts of 6947 rows 130, with 64 165, with
+// 512 134; from 8 bits 148, 190 and 154.
 constexpr int kFewFixed = 128, kFewFixed8 = 320, kManyFixed = 256;
-constexpr int kFewLeast = 256, kManyLeast = 256;     // the least range of a workgroup
-constexpr int kFewWhole = 192, kManyWhole = 768;     // a tile of no more keys is not cut
+// The least range of a workgroup.  Few: one token over 4999 keys 18.7, with 128
+// 22.1, with 512 23.0.  Many: 128 and 512 within 1.5%.
+constexpr int kFewLeast = 256, kManyLeast = 256;
+// A tile of no more keys is not cut.  Few: 64 requests behind a shared prefix 73,
+// with 64 76, with 768 73; 256 decode within 1%.  Many: 256 requests behind 8 prefixes
+// 96, with 2048 116; queries to 300 to 1500 keys of another sequence 34, with 256
+// 35.5, with 2048 37.
+constexpr int kFewWhole = 192, kManyWhole = 768;
 constexpr int kFewStep = 128, kManyStep = 64;        // keys of a round
 constexpr int kJoinGroups = 512;                     // workgroups that join pieces of many rows
 // A workspace begins with a ticket for every workgroup, 0 between calls, and 16
