@@ -1,5 +1,6 @@
 """Calls of the paged cache's operators at the edge of what they accept: refusals, scales of 0 and not finite, and
 the second, careful way of the many-row kernel in every form.  Definition and bounds are those of test_gpu_attend.py."""
+import copy
 import math
 
 import pytest
@@ -164,3 +165,86 @@ def test_prefix_starts_that_make_no_sense_stay_inside():
         want = x.want()
         assert (ws[:4096] == 0).all()
         near(x.call(out=out[4:-4], ws=ws).out, want[0], want[2], "afterwards")
+
+
+# ---------------------------------------------------------------- forms and sizes that no other test has
+@pytest.mark.parametrize("rows", [[7, 0, 130, 1, 40], [2, 1, 0, 3, 2]])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefixes_of_queries_to_another_sequence(rows, cache, dim):
+    """Rows that all see every key of their prefix and their request, against a request of its own for each row."""
+    lens = [40, 3, 900, 0, 129]
+    b = Batch(90, rows, lens, dim=dim, cache=cache, prefixes=((300, 1), (70, 3)), first=1)
+    each = copy.copy(b)
+    of = [r for r, count in enumerate(rows) for _ in range(count)]
+    each.rows, each.lens, each.pages = [1] * len(of), [lens[r] for r in of], b.pages[of].contiguous()
+    each.first, each.prefixes = rows[0], ((300, rows[1]), (70, sum(rows[2:])))
+    check(b, "not causal", causal=False, want=each.want())
+
+
+def small_cache(g, pages, page, dim):
+    return [torch.randn(pages, page, 1, dim, generator=g, device="cuda").bfloat16() for _ in range(2)]
+
+
+def one_page(q, k, v, mask):
+    """(out, bound) in 64 bits of rows that have keys k [rows, keys, dim] of their own; the bound as in test_gpu_attend.py,
+    scores of 16 products of normal values being off by less than 2^-16."""
+    q, k, v = q.double(), k.double()[:, None], v.double()[:, None]
+    s = ((q[:, :, None] * k).sum(dim=3) * q.shape[2] ** -0.5).masked_fill(~mask[:, None], -math.inf)
+    p = torch.where(mask[:, None], torch.softmax(s, dim=2), 0.0)[..., None]
+    o = (p * v).sum(dim=2)
+    return o, 2.0 ** -8 * o.abs() + (p * v.abs()).sum(dim=2) * (1.01 * 2.0 ** -8 + 2.0 ** -14)
+
+
+def test_the_most_requests_and_prefixes():
+    g, n, page, dim = gen(91), 1 << 16, 16, 16
+    kc, vc = small_cache(g, 1000, page, dim)
+    pages = torch.randint(0, 1000, (n, 1), generator=g, device="cuda").int()
+    lens = torch.randint(0, page + 1, (n,), generator=g, device="cuda").int()
+    q = torch.randn(n, 2, dim, generator=g, device="cuda").bfloat16()
+    k, v = kc[pages[:, 0].long(), :, 0], vc[pages[:, 0].long(), :, 0]
+    mask = torch.arange(page, device="cuda")[None] < lens[:, None]
+    want = one_page(q, k, v, mask)
+    near(step.paged_attention(q, kc, vc, pages, lens).out, *want, "tokens")
+    each = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    near(step.paged_attention(q, kc, vc, pages, lens, starts=each, max_rows=200).out, *want, "the other kernel")
+    prefix = step.Prefixes(pages.flip(0).contiguous(), lens.flip(0).contiguous(), each)
+    want = one_page(q, *(torch.cat([x.flip(0), x], dim=1) for x in (k, v, mask)))
+    near(step.paged_attention(q, kc, vc, pages, lens, prefix=prefix).out, *want, "prefixes")
+    with pytest.raises(LoraError):
+        step.paged_attention(torch.cat([q, q[:1]]), kc, vc, torch.cat([pages, pages[:1]]), torch.cat([lens, lens[:1]]))
+
+
+def test_the_most_tokens():
+    g, n, dim = gen(92), 1 << 20, 16
+    kc, vc = small_cache(g, 9, 16, dim)
+    q = torch.randn(n, 1, dim, generator=g, device="cuda").bfloat16()
+    pages, lens, starts = ints([[3, 1, 8], [0, 2, 4]]), ints([37, 5]), ints([0, n // 2 + 3, n])
+    for hint in (n, 1):
+        r = step.paged_attention(q, kc, vc, pages, lens, starts=starts, max_rows=hint, causal=False)
+        for b, (a, z) in enumerate(((0, n // 2 + 3), (n // 2 + 3, n))):
+            k, v = (c[pages[b].long()].flatten(0, 1)[None, :lens[b].item(), 0] for c in (kc, vc))
+            want = one_page(q[a:z], k, v, torch.ones(1, k.shape[1], dtype=torch.bool, device="cuda"))
+            near(r.out[a:z], *want, f"request {b}")
+    r = step.paged_attention(q, kc, vc, pages, lens, starts=starts, max_rows=n)
+    assert (r.out[:n // 2 + 3 - 37] == 0).all() and (r.out[n // 2 + 3:n - 5] == 0).all() and (r.out[n - 1] != 0).any()
+    kc, vc = (torch.zeros(n // 16, 16, 1, dim, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    place = torch.randperm(n, generator=g, device="cuda").int()
+    step.kv_append(q, -q, kc, vc, place)
+    assert torch.equal(kc.flatten(0, 1)[place.long()], q) and torch.equal(vc.flatten(0, 1)[place.long()], -q)
+
+
+def test_rows_past_32_bits():
+    """Queries and results of more than 2^32 bytes and 2^31 elements."""
+    g, n, heads, kv, dim = gen(93), (1 << 17) + 5, 160, 10, 128
+    q = torch.randn(n, heads, dim, generator=g, device="cuda", dtype=torch.bfloat16)
+    kc, vc = (torch.randn(5, 16, kv, dim, generator=g, device="cuda").bfloat16() for _ in range(2))
+    lens, starts = ints([70]), ints([0, n])
+    r = step.paged_attention(q, kc, vc, ints([list(range(5))]), lens, starts=starts, max_rows=n, causal=False)
+    for row in (0, n // 2, n - 200, n - 1):
+        k, v = (c.flatten(0, 1)[:70].double().repeat_interleave(heads // kv, dim=1) for c in (kc, vc))
+        x = q[row].double()
+        p = torch.softmax((k * x).sum(dim=2) * dim ** -0.5, dim=0)[:, :, None]
+        o = (p * v).sum(dim=0)
+        # (p's and the result's rounding, and scores of 128 products of magnitudes below 30 in all: 130 x 30 x 2^-24)
+        near(r.out[row], o, 2.0 ** -8 * o.abs() + (p * v.abs()).sum(dim=0) * (1.01 * 2.0 ** -8 + 2.0 ** -10), f"row {row}")
