@@ -6,7 +6,7 @@
 // in fp32, rounded once to bf16 or, over the head's scale, to e4m3.  A thread
 // takes one unit: 16 bytes of a head, or the two 16 bytes whose halves pair up,
 // so q may be turned in place.  Bound by memory traffic for many tokens (6947 with
-// 32 query and 8 key heads of 128: 41 us, 4.3 TB/s) and by latency for few (one
+// 32 query and 8 key heads of 128: 41 us, 4.2 TB/s) and by latency for few (one
 // token: 3 us, and 10 more of host time).
 #include "attend_kernels.h"
 #include "common.h"

@@ -10,10 +10,10 @@
 // part of LDS into the layout of the matrix cores, without a barrier.  The four
 // waves of a workgroup take the tiles of 32 keys in turn and their results are
 // joined in LDS.  256 tokens over 64 to 4096 keys, 8 key heads of 128: 178 us, 5.7
-// TB/s; from 8 bits 102 us, 4.9 TB/s, where the time that a tile costs beside its
+// TB/s; from 8 bits 103 us, 4.9 TB/s, where the time that a tile costs beside its
 // keys counts more (keys for two rounds ahead in registers, and the next tile's
 // first keys sent before the end of a tile, changed neither).  One token over 4999
-// keys: 16 us, the latency of lengths, pages, keys and the join of 20 pieces.
+// keys: 17 us, the latency of lengths, pages, keys and the join of 20 pieces.
 //
 // S^T = K Q^T gives a lane one row of q and 8 of the 32 keys, and p as it lies
 // there is the operand that O^T = V^T P^T wants, with the keys of the product

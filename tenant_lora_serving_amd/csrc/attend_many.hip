@@ -9,8 +9,9 @@
 // matrix cores, the exponentials and LDS reads.  Each of the four waves holds 32
 // rows; all read the keys and values from LDS, two buffers in turn, the next 64
 // keys on their way meanwhile, one barrier a round.  2048 rows of 4 requests over
-// 4000 to 24000 keys, 32 heads of 128: 711 us in all, 0.8 PFLOP/s, matrix
-// instructions busy 48% of the cycles; whole prompts of 6947 rows: 145 us, of
+// 4000 to 24000 keys, 32 heads of 128: 712 us in all, 0.8 PFLOP/s, matrix
+// instructions busy 50% of the cycles and vector ones 53%, waves waiting 26% of
+// their time; whole prompts of 6947 rows: 144 us, of
 // which 14 join pieces.
 //
 // S^T = K Q^T gives a lane one row of q and half of the keys, and p as it lies
